@@ -435,6 +435,111 @@ tbg_status tbg_conv2d_fwd(const tbg_conv2d_shape* shape, float alpha, const void
                           void* y, int64_t ldy, tbg_dtype y_dtype, const tbg_gemm_config* cfg, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/* ---- products over ragged groups ------------------------------------------------------------
+ * The rows of one matrix fall into groups (the tokens of each expert, the documents of a batch),
+ * each with a matrix of its own.
+ *   offsets   device memory, int32, groups + 1 values, 4-byte aligned: group e holds rows
+ *             offsets[e] .. offsets[e+1]-1.  They must not descend and must lie in 0..M; groups
+ *             may be empty, and rows before offsets[0] or from offsets[groups] on belong to none.
+ *             They are read on `stream` when the work runs, so a captured graph replays with the
+ *             offsets then in memory.  Values outside 0..M are taken as the nearer bound and a
+ *             descending pair as an empty group: nothing outside the operands is read or written
+ *             (but rows that two groups then share hold either's result).
+ * Limits: M, N and K (P and Q) up to 2^30, groups up to 4096, leading dimensions of 16-bit
+ * operands below 2^22 elements. */
+
+/* Workspace bytes tbg_gemm_grouped needs for these operands (only compared against 16-byte
+ * boundaries, never dereferenced): A is repacked when lda % 8, K % 8 or A % 16 is non-zero; B
+ * (N×K) likewise with ldb, and when stride_b % 8 is non-zero (groups > 1); B (K×N) when ldb % 8,
+ * stride_b % 8 or B % 16 is non-zero.  0 for non-positive sizes or another type. */
+size_t tbg_gemm_grouped_workspace_query(int64_t groups, int64_t M, int64_t N, int64_t K, tbg_dtype ab_dtype,
+                                        const void* A, int64_t lda, const void* B, int64_t ldb, int64_t stride_b,
+                                        tbg_b_layout bl);
+
+/* C[r] <- alpha·A[r]·B_e + beta·C[r] for every row r of every group e ([GEMM] "Il conto", one
+ * product per group in a single launch).
+ *   A          TBG_BF16 or TBG_F16 (ab_dtype), row-major M×K, lda >= K.
+ *   B          the same type; B_e starts stride_b elements after B_(e-1) and is stored K×N
+ *              (TBG_B_KN, ldb >= N) or N×K (TBG_B_NK, ldb >= K).  The product with the other
+ *              layout of the same memory is the gradient of the rows.
+ *   C          TBG_F32 or ab_dtype, row-major M×N, ldc >= N, rounded once to nearest even.  Rows of
+ *              no group are left as they were.  C must not overlap A, B or the workspace.
+ *   alpha, beta  as tbg_gemm_ex: beta == 0 does not read C, alpha == 0 reads neither A nor B.
+ *   workspace  tbg_gemm_grouped_workspace_query(...) bytes, 256-byte aligned; NULL when 0.  With
+ *              twice the need, successive calls repack into its two halves alternately.  Calls that
+ *              may run at once (two streams, two captured graphs) need a workspace each.
+ * groups == 0, M == 0 or N == 0 is a no-op; K == 0 gives beta·C (zeros when beta == 0).
+ * Returns INVALID_VALUE (negative sizes, ld or stride below its minimum, null pointers, bad
+ * enum, C type), MISALIGNED (offsets, workspace), UNSUPPORTED (limits), OUT_OF_RANGE (workspace
+ * too small), NO_DEVICE / HIP. */
+tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int32_t* offsets, float alpha,
+                            const void* A, int64_t lda, const void* B, int64_t ldb, int64_t stride_b, tbg_b_layout bl,
+                            tbg_dtype ab_dtype, float beta, void* C, int64_t ldc, tbg_dtype c_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Workspace bytes tbg_gemm_grouped_wgrad needs: X is repacked when ldx % 8 or X % 16 is non-zero,
+ * Y likewise. */
+size_t tbg_gemm_grouped_wgrad_workspace_query(int64_t groups, int64_t M, int64_t P, int64_t Q, tbg_dtype ab_dtype,
+                                              const void* X, int64_t ldx, const void* Y, int64_t ldy);
+
+/* C_e <- alpha·X_eᵀ·Y_e + beta·C_e, X_e and Y_e the rows of group e: the gradient of B_e, from the
+ * rows A and the gradient of C of tbg_gemm_grouped (X = A, Y = dC gives it stored K×N; X = dC,
+ * Y = A stored N×K).  The sum over a group's rows is held in fp32.
+ *   X, Y       TBG_BF16 or TBG_F16 (ab_dtype), row-major M×P (ldx >= P) and M×Q (ldy >= Q).
+ *   C          TBG_F32 or ab_dtype; C_e row-major P×Q, ldc >= Q, stride_c elements after C_(e-1).
+ *              Every C_e is written: an empty group's becomes beta·C_e (zeros when beta == 0).
+ *   alpha, beta, workspace, errors as tbg_gemm_grouped; beta == 1 adds to a gradient held in C.
+ * groups == 0, P == 0 or Q == 0 is a no-op. */
+tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t Q, const int32_t* offsets,
+                                  float alpha, const void* X, int64_t ldx, const void* Y, int64_t ldy,
+                                  tbg_dtype ab_dtype, float beta, void* C, int64_t ldc, int64_t stride_c,
+                                  tbg_dtype c_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- microscaled 4-bit data -------------------------------------------------------------------
+ * Values in blocks of 32 along a row share a scale (the OCP Microscaling Formats specification,
+ * version 1.0, "MXFP4"): value = E2M1(code) · 2^(scale byte - 127); code 0..7 stands for 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6, codes 8..15 for their negatives; scale byte 255 makes the block NaN.
+ * A matrix of `rows` rows and K columns (K a multiple of 32) is held as
+ *   codes    two per byte, the lower nibble first: rows of K/2 bytes, ld_codes bytes apart;
+ *   scales   one byte per block: rows of K/32 bytes, ld_scales bytes apart;
+ * both 16-byte aligned with pitches that are multiples of 16.  Scale bytes of a row past K/32 do
+ * not reach any result (the bytes up to the next multiple of 4 are read). */
+
+/* Quantise X (rows×cols, TBG_F32, TBG_BF16 or TBG_F16, row-major at pitch ldx elements, any
+ * alignment of whole elements) to rows of K = cols rounded up to 32 columns; the columns past cols
+ * are zeros.  Per block, with m the largest magnitude: scale exponent clamp(floor(log2 m) - 2,
+ * -127, 127), codes rounded to nearest even and clipped to magnitude 6.  A block that holds a NaN
+ * or an infinity gets scale byte 255 and zero codes.  rows == 0 or cols == 0 is a no-op.
+ * Returns INVALID_VALUE (negative sizes, pitches too small, null pointers, type), MISALIGNED (X off
+ * its element size; codes, scales or their pitches off 16), UNSUPPORTED (cols above 2^30),
+ * NO_DEVICE / HIP. */
+tbg_status tbg_mx4_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, tbg_dtype x_dtype, void* codes,
+                            int64_t ld_codes, void* scales, int64_t ld_scales, void* stream);
+
+/* The values of the first cols columns, written to X (rounded to X's type where it cannot hold
+ * them).  Arguments and errors as tbg_mx4_quantize. */
+tbg_status tbg_mx4_dequantize(int64_t rows, int64_t cols, const void* codes, int64_t ld_codes, const void* scales,
+                              int64_t ld_scales, void* X, int64_t ldx, tbg_dtype x_dtype, void* stream);
+
+/* C <- alpha·A·Bᵀ + beta·C for 4-bit A (M×K) and B (stored N×K) on the scaled matrix instruction,
+ * fp32 accumulation, C TBG_F32 or TBG_BF16 (row-major, ldc >= N).  alpha, beta as tbg_gemm_ex.  K is
+ * a multiple of 32 (columns that quantisation added are zeros and change nothing).
+ * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.  Limits: sizes up to 2^30, pitches of codes
+ * below 2^23 bytes.
+ * Returns INVALID_VALUE (negative sizes, K % 32, pitches too small, null pointers, C type),
+ * MISALIGNED (codes, scales or pitches off 16), UNSUPPORTED (limits), NO_DEVICE / HIP. */
+tbg_status tbg_mx4_gemm(int64_t M, int64_t N, int64_t K, float alpha, const void* A, int64_t lda, const void* A_scales,
+                        int64_t ld_as, const void* B, int64_t ldb, const void* B_scales, int64_t ld_bs, float beta,
+                        void* C, int64_t ldc, tbg_dtype c_dtype, void* stream);
+
+/* tbg_mx4_gemm over ragged groups: C[r] <- alpha·A[r]·B_eᵀ + beta·C[r] for the rows r of group e.
+ * B_e's codes start stride_b bytes after B_(e-1)'s and its scales stride_bs bytes after, both
+ * multiples of 16.  offsets, groups and rows of no group as tbg_gemm_grouped. */
+tbg_status tbg_mx4_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int32_t* offsets, float alpha,
+                                const void* A, int64_t lda, const void* A_scales, int64_t ld_as, const void* B,
+                                int64_t ldb, int64_t stride_b, const void* B_scales, int64_t ld_bs, int64_t stride_bs,
+                                float beta, void* C, int64_t ldc, tbg_dtype c_dtype, void* stream);
+
 /* Static text for a status code. */
 const char* tbg_status_string(tbg_status s);
 

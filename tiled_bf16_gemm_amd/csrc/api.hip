@@ -12,6 +12,7 @@
 #include <mutex>
 #include <string>
 
+#include "api_util.hpp"
 #include "launch.hpp"
 #include "tbg.h"
 #include "tbg_desc.hpp"
@@ -23,7 +24,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
-tbg_status fail(tbg_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+namespace tbg {
+
 tbg_status fail(tbg_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -33,6 +37,16 @@ tbg_status fail(tbg_status s, const char* fmt, ...) {
   g_last_error = buf;
   return s;
 }
+
+}  // namespace tbg
+
+namespace {
+
+using tbg::check_device;
+using tbg::fail;
+using tbg::log_choice;
+using tbg::round_up;
+using tbg::rows_dword_aligned;
 
 int elsize_of(int dtype) {
   switch (dtype) {
@@ -52,9 +66,11 @@ uint32_t swizzle_span(int mode) {
   }
 }
 
-// A usable device: the current HIP device must be gfx950.  Checked once per device id, which
-// also records the device's compute-unit count (returned through num_cus when given).
-tbg_status check_device(int* num_cus = nullptr) {
+}  // namespace
+
+namespace tbg {
+
+tbg_status check_device(int* num_cus) {
   int dev = -1;
   int count = 0;
   if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
@@ -85,6 +101,10 @@ tbg_status check_device(int* num_cus = nullptr) {
   return TBG_OK;
 }
 
+}  // namespace tbg
+
+namespace {
+
 bool valid_desc(const tbg_tensor_desc* d, const DescImpl** out) {
   if (!d) return false;
   const DescImpl* di = reinterpret_cast<const DescImpl*>(d);
@@ -108,8 +128,10 @@ int64_t conv_out_dim(int64_t in, int64_t pad_lo, int64_t pad_hi, int64_t stride,
   return span / stride + 1;
 }
 
-// TBG_LOG set to anything but "" or "0": every GEMM and convolution call reports the kernel
-// configuration it launches on stderr (read once per process).
+}  // namespace
+
+namespace tbg {
+
 void log_choice(const char* fmt, ...) {
   static const bool on = [] {
     const char* v = getenv("TBG_LOG");
@@ -124,13 +146,20 @@ void log_choice(const char* fmt, ...) {
   va_end(ap);
 }
 
-// Whether the epilogue may store whole 16-byte pieces of C's rows (8-byte pieces in the scaled
-// bf16 path): gfx9's multi-dword memory instructions need only dword-aligned addresses, so C's
-// base and its row pitch in bytes must be multiples of 4 (every fp32 C at a 4-byte aligned base;
-// a bf16 C when ldc is even).  Otherwise the epilogue stores element by element.
-int rows_dword_aligned(const void* C, int64_t ldc, tbg_dtype c_dtype) {
-  return (((uintptr_t)C) % 4 == 0) && ((ldc * (c_dtype == TBG_BF16 ? 2 : 4)) % 4 == 0);
+int rows_dword_aligned(const void* C, int64_t ldc, int elsize) {
+  return (((uintptr_t)C) % 4 == 0) && ((ldc * elsize) % 4 == 0);
 }
+
+uint8_t* repack_area(void* workspace, size_t workspace_bytes, size_t need) {
+  static std::atomic<uint32_t> calls{0};
+  const size_t half = (size_t)round_up((int64_t)need, 256);
+  if (need == 0 || workspace_bytes < 2 * half) return (uint8_t*)workspace;
+  return (uint8_t*)workspace + (calls.fetch_add(1, std::memory_order_relaxed) & 1u) * half;
+}
+
+}  // namespace tbg
+
+namespace {
 
 int env_int(const char* name, int dflt) {
   const char* v = getenv(name);
@@ -452,20 +481,7 @@ namespace {
 
 constexpr int64_t kMaxLd = (1ll << 22) - 1;
 
-int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
-// Where a call's repacked operands go in the caller's workspace.  A workspace of at least twice
-// the need (each half 256-byte aligned) is used by halves, alternately from call to call (one
-// counter for the process): a repack that overwrites the copy which the previous product has
-// just read runs much slower on MI355X (the 3001×2049×777 operands: ≈8.5 µs, against ≈4.7 µs
-// into the other half; kernel trace), and consecutive products usually share one workspace.
-// The half only moves where the repack lands, never what the product computes.
-uint8_t* repack_area(void* workspace, size_t workspace_bytes, size_t need) {
-  static std::atomic<uint32_t> calls{0};
-  const size_t half = (size_t)round_up((int64_t)need, 256);
-  if (need == 0 || workspace_bytes < 2 * half) return (uint8_t*)workspace;
-  return (uint8_t*)workspace + (calls.fetch_add(1, std::memory_order_relaxed) & 1u) * half;
-}
+using tbg::repack_area;
 
 struct PackPlan {
   bool pack_a = false, pack_b = false;
@@ -672,7 +688,7 @@ tbg_status gemm_fp8_impl(int64_t M, int64_t N, int64_t K, float alpha, const voi
   p.K = (int)(K > 0 ? k16 / 2 : 0);
   p.kchunks = K > 0 ? (int)(k16 / 16) : 0;  // K = 0: every copy lane masked, A and B never read
   p.group_m = 8;
-  p.vec_store = rows_dword_aligned(C, ldc, c_dtype);
+  p.vec_store = rows_dword_aligned(C, ldc, elsize_of(c_dtype));
   p.alpha = alpha;
   p.beta = beta;
   p.scaled = scaled ? 1 : 0;
@@ -816,7 +832,7 @@ tbg_status gemm_impl(int64_t M, int64_t N, int64_t K, float alpha, const void* A
   // 16384×14336×4096; 2, 16 and 32 are slower.
   p.group_m = env_int("TBG_GROUP_M", 4);
   if (p.group_m < 1) p.group_m = 1;
-  p.vec_store = rows_dword_aligned(C, ldc, c_dtype);
+  p.vec_store = rows_dword_aligned(C, ldc, elsize_of(c_dtype));
   p.alpha = alpha;
   p.beta = beta;
   p.scaled = scaled ? 1 : 0;
@@ -1066,7 +1082,7 @@ tbg_status tbg_conv2d_fwd(const tbg_conv2d_shape* shape, float alpha, const void
   cp.g.K = (int)(ldw);
   cp.g.kchunks = (int)(ldw / 8);
   cp.g.group_m = 8;
-  cp.g.vec_store = rows_dword_aligned(y, ldy, y_dtype);
+  cp.g.vec_store = rows_dword_aligned(y, ldy, elsize_of(y_dtype));
   cp.g.alpha = alpha;
   cp.g.beta = beta;
   cp.g.scaled = scaled ? 1 : 0;

@@ -40,6 +40,7 @@ namespace tbg {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
@@ -261,19 +262,40 @@ __device__ __forceinline__ int park_xor(int r) {
   return (r >> 2) & 3;  // CPR == 4
 }
 
+// Four fp32 values rounded to nearest even in C's 16-bit type: OUT 1 bf16, 2 fp16.
+template <int OUT>
+struct Half4;
+template <>
+struct Half4<1> {
+  typedef bf16x4_t vec;
+  typedef __bf16 elem;
+};
+template <>
+struct Half4<2> {
+  typedef f16x4_t vec;
+  typedef _Float16 elem;
+};
+template <int OUT>
+__device__ __forceinline__ typename Half4<OUT>::vec round4(const f32x4_t& v) {
+  typename Half4<OUT>::vec h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = (typename Half4<OUT>::elem)v[e];
+  return h;
+}
+
 // The epilogue: C leaves through LDS as whole rows.  A lane holds C[m][n..n+3] of each fragment,
 // so storing fragments directly would write 16 rows × 32 bytes per instruction.  Instead each
 // wave parks its block (in one or two bands of rows) in its own quarter of the now idle ring,
 // then reads it back as 16-byte pieces of whole rows, so every store instruction writes whole
 // row segments.  Whole-row stores are non-temporal: C is written once and not read again here,
-// so it should not push operand tiles out of the caches.  With SCALED the park keeps the fp32
+// so it should not push operand tiles out of the caches.  OUT: 0 fp32, 1 bf16, 2 fp16.  With SCALED the park keeps the fp32
 // sums and each piece becomes alpha·S + beta·C_old (C_old read only when beta != 0) before it is
 // rounded to C's type ("GEMM" page, tensor-core section: C <- alpha·A·B + beta·C).
 template <class T, int OUT, int SCALED>
 __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[T::FN][T::FM], uint8_t* park, const GemmParams& p,
                                           int row0, int col0, int lane) {
-  constexpr int ES = OUT == 1 ? 2 : 4;                     // element size of C
-  constexpr int PES = (OUT == 1 && !SCALED) ? 2 : 4;       // element size in the park
+  constexpr int ES = OUT != 0 ? 2 : 4;                     // element size of C
+  constexpr int PES = (OUT != 0 && !SCALED) ? 2 : 4;       // element size in the park
   constexpr int RowBytes = T::TN * PES;
   constexpr int CPR = RowBytes / 16;
   constexpr int EPC = 16 / PES;  // elements per 16-byte park chunk
@@ -292,12 +314,10 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[T::FN][T::FM], u
       for (int fn = 0; fn < T::FN; ++fn) {
         const int r = 16 * f + (lane & 15);
         const f32x4_t v = acc[fn][band * BandFM + f];
-        if (PES == 2) {
+        if constexpr (PES == 2) {
           const int c = 2 * fn + (lane >> 5);
-          bf16x4_t h;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = (__bf16)v[e];
-          *(bf16x4_t*)(park + r * RowBytes + ((c ^ park_xor<CPR>(r)) << 4) + ((lane >> 4) & 1) * 8) = h;
+          const auto h = round4<OUT>(v);
+          *(typename Half4<OUT>::vec*)(park + r * RowBytes + ((c ^ park_xor<CPR>(r)) << 4) + ((lane >> 4) & 1) * 8) = h;
         } else {
           const int c = 4 * fn + (lane >> 4);
           *(f32x4_t*)(park + r * RowBytes + ((c ^ park_xor<CPR>(r)) << 4)) = v;
@@ -320,7 +340,7 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[T::FN][T::FM], u
 #pragma unroll
           for (int e = 0; e < EPC; ++e) {
             if (gn + e >= p.N) continue;
-            if (OUT == 1) ((uint16_t*)dst)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            if (OUT != 0) ((uint16_t*)dst)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
             else ((uint32_t*)dst)[e] = w[e];
           }
         }
@@ -336,6 +356,10 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[T::FN][T::FM], u
               old[1] = __uint_as_float(o.x & 0xFFFF0000u);
               old[2] = __uint_as_float(o.y << 16);
               old[3] = __uint_as_float(o.y & 0xFFFF0000u);
+            } else if (OUT == 2) {
+              const f16x4_t o = *(const f16x4_t*)dst;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) old[e] = (float)o[e];
             } else {
               const uint4 o = *(const uint4*)dst;
               old[0] = __uint_as_float(o.x);
@@ -347,22 +371,22 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[T::FN][T::FM], u
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (gn + e >= p.N) continue;
-              old[e] = OUT == 1 ? __uint_as_float((uint32_t)((const uint16_t*)dst)[e] << 16) : ((const float*)dst)[e];
+              old[e] = OUT == 1   ? __uint_as_float((uint32_t)((const uint16_t*)dst)[e] << 16)
+                       : OUT == 2 ? (float)((const _Float16*)dst)[e]
+                                  : ((const float*)dst)[e];
             }
           }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = p.beta != 0.f ? p.alpha * x[e] + p.beta * old[e] : p.alpha * x[e];
-        if (OUT == 1) {
-          bf16x4_t h;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = (__bf16)x[e];
+        if constexpr (OUT != 0) {
+          const auto h = round4<OUT>(f32x4_t{x[0], x[1], x[2], x[3]});
           if (whole) {
-            *(bf16x4_t*)dst = h;
+            *(typename Half4<OUT>::vec*)dst = h;
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (gn + e < p.N) ((__bf16*)dst)[e] = h[e];
+              if (gn + e < p.N) ((typename Half4<OUT>::elem*)dst)[e] = h[e];
           }
         } else {
           if (whole) {

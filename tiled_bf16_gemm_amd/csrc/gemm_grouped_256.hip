@@ -1,0 +1,7 @@
+// Ragged products, 256×256 tiles.
+#include "gemm_grouped_instances.hpp"
+
+namespace tbg {
+template hipError_t launch_grouped_tile<256, 2>(const GroupedParams&, int, int, int, unsigned, hipStream_t);
+template hipError_t launch_wgrad_tile<256, 2>(const GroupedParams&, int, int, unsigned, hipStream_t);
+}  // namespace tbg

@@ -113,6 +113,37 @@ hipError_t launch_pack_jobs(const PackJob* jobs, int n, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Equal repacks of matrices at a fixed distance: workgroup row y takes matrix y.
+__global__ void __launch_bounds__(256) pack_groups_kernel(PackJob j, uint32_t chunks, uint32_t cpr, FastDiv div,
+                                                          int64_t group_stride) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= chunks) return;
+  j.src += (int64_t)blockIdx.y * group_stride;
+  j.dst += (int64_t)blockIdx.y * j.rows * j.ld_dst;
+  const uint32_t r = fast_div(i, div), c = i - r * cpr;
+  *(uint4*)(j.dst + (uint64_t)r * (uint64_t)j.ld_dst + c * 16u) = pack_chunk(j, r, c * 16u);
+}
+
+hipError_t launch_pack_groups(const PackJob& j, int64_t groups, int64_t group_stride, hipStream_t stream) {
+  if (j.ld_dst >= (1ll << 31) || j.row_bytes > j.ld_dst || groups > 65535) return hipErrorInvalidValue;
+  const uint32_t cpr = (uint32_t)(j.ld_dst / 16);
+  const uint64_t chunks = (uint64_t)cpr * (uint64_t)j.rows;
+  if (chunks == 0 || groups <= 0) return hipSuccess;
+  if (chunks >= (1ull << 32) - 256) {  // 64 GiB a matrix: one launch each
+    for (int64_t g = 0; g < groups; ++g) {
+      PackJob one = j;
+      one.src += g * group_stride;
+      one.dst += g * j.rows * j.ld_dst;
+      const hipError_t e = launch_pack_jobs(&one, 1, stream);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  hipLaunchKernelGGL(pack_groups_kernel, dim3((uint32_t)((chunks + 255) / 256), (uint32_t)groups), dim3(256), 0,
+                     stream, j, (uint32_t)chunks, cpr, make_fast_div(cpr), group_stride);
+  return hipGetLastError();
+}
+
 namespace {
 
 struct GemmVariant {

@@ -112,6 +112,59 @@ struct PackJob {
 };
 // Runs n (1 or 2) repacks in one launch.
 hipError_t launch_pack_jobs(const PackJob* jobs, int n, hipStream_t stream);
+// `groups` repacks like `j`, their sources group_stride bytes apart, their results dense.
+hipError_t launch_pack_groups(const PackJob& j, int64_t groups, int64_t group_stride, hipStream_t stream);
+// Arguments of the ragged products (gemm_grouped.hpp).  Pitches of A and B in bytes, of C in
+// elements; group e holds rows offsets[e] .. offsets[e+1]-1 (device memory) of `rows`.
+//   rows product:     A rows × K, B_e at B + e·stride_b, C rows × N
+//   weight gradient:  A rows × M, B rows × N, C_e M × N at C + e·stride_c (elements)
+struct GroupedParams {
+  const uint8_t* A;
+  const uint8_t* B;
+  void* C;
+  const int32_t* offsets;
+  int64_t lda, ldb, stride_b, ldc, stride_c;
+  int groups, rows;
+  int M, N, K;
+  int tiles_m, tiles_n, group_m;
+  int vec_store;
+  float alpha, beta;
+  int scaled;
+};
+// in: 0 bf16, 1 fp16; out: 0 fp32, 1 bf16, 2 fp16 (a 16-bit output has the input's type).  Tiles
+// 256×256, 128×128, 64×64; they fill the tile counts and the grid.
+hipError_t launch_grouped(GroupedParams p, int bm, int bn, int in, int b_layout, int out, hipStream_t stream);
+hipError_t launch_wgrad(GroupedParams p, int bm, int bn, int in, int out, hipStream_t stream);
+// Upper bound of the tiles of height bm over any split of `rows` rows into `groups` groups.
+inline int64_t ragged_tiles_bound(int64_t rows, int64_t groups, int64_t bm) {
+  const int64_t g = groups < rows ? groups : rows;
+  return (rows + g * (bm - 1)) / bm;
+}
+
+// Arguments of the 4-bit conversions (mx4_quantize.hip): pitches in bytes; per_row = 4 units of 8
+// values for every block of 32 (ceil(cols / 32) blocks); units and div are filled by the launcher.
+struct Mx4Params {
+  void* x;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ldx, ld_codes, ld_scales, cols;
+  uint32_t per_row, units;
+  FastDiv div;
+};
+// dt: 0 fp32, 1 bf16, 2 fp16 (the type of x)
+hipError_t launch_mx4_quantize(const Mx4Params& p, int64_t rows, int dt, hipStream_t stream);
+hipError_t launch_mx4_dequantize(const Mx4Params& p, int64_t rows, int dt, hipStream_t stream);
+
+// Arguments of the 4-bit products (gemm_mx4.hpp): g.A and g.B hold codes (pitches in bytes, K a
+// multiple of 32), As and Bs the scale bytes; g.offsets null: one dense product of g.rows rows.
+struct Mx4GemmParams {
+  GroupedParams g;
+  const uint8_t* As;
+  const uint8_t* Bs;
+  int64_t ld_as, ld_bs, stride_bs;
+};
+hipError_t launch_mx4_gemm(Mx4GemmParams p, int bm, int bn, int out_bf16, hipStream_t stream);
+
 // fp8 GEMM (gemm_fp8.hpp): p in units of two fp8 values (lda, ldb, K, kchunks as for 16-bit data
 // of half the width); fmt 0 E4M3, 1 E5M2; tiles 256×256, 128×128, 64×64.
 hipError_t launch_fp8(GemmParams p, int bm, int bn, int fmt, int out_bf16, hipStream_t stream);
