@@ -422,7 +422,7 @@ def gemm_status(*args, **kwargs) -> int:
 
 def gemm_grouped_workspace_query(groups: int, M: int, N: int, K: int, ab_dtype, A: int, lda: int, B: int, ldb: int,
                                  stride_b: int, b_layout="kn") -> int:
-    return int(_lib.tbg_gemm_grouped_workspace_query(groups, M, N, K, _enum(DTYPES, ab_dtype), int(A), lda, int(B), ldb,
+    return int(_lib.tbg_gemm_grouped_workspace_query(groups, M, N, K, _enum(DTYPES, ab_dtype), A, lda, B, ldb,
                                                      stride_b, _enum(B_LAYOUTS, b_layout)))
 
 
@@ -430,53 +430,53 @@ def gemm_grouped(groups: int, M: int, N: int, K: int, offsets: int, alpha: float
                  stride_b: int, b_layout, ab_dtype, beta: float, C: int, ldc: int, c_dtype, workspace: int = 0,
                  workspace_bytes: int = 0, stream: Optional[int] = None) -> None:
     """tbg_gemm_grouped: C[r] = alpha·A[r]·B_e + beta·C[r] for the rows r of every group e."""
-    _check(_lib.tbg_gemm_grouped(groups, M, N, K, int(offsets), float(alpha), int(A), lda, int(B), ldb, stride_b,
-                                 _enum(B_LAYOUTS, b_layout), _enum(DTYPES, ab_dtype), float(beta), int(C), ldc,
-                                 _enum(DTYPES, c_dtype), int(workspace), int(workspace_bytes), stream or None))
+    _check(_lib.tbg_gemm_grouped(groups, M, N, K, offsets, alpha, A, lda, B, ldb, stride_b,
+                                 _enum(B_LAYOUTS, b_layout), _enum(DTYPES, ab_dtype), beta, C, ldc,
+                                 _enum(DTYPES, c_dtype), workspace, workspace_bytes, stream or None))
 
 
 def gemm_grouped_wgrad_workspace_query(groups: int, M: int, P: int, Q: int, ab_dtype, X: int, ldx: int, Y: int,
                                        ldy: int) -> int:
-    return int(_lib.tbg_gemm_grouped_wgrad_workspace_query(groups, M, P, Q, _enum(DTYPES, ab_dtype), int(X), ldx,
-                                                           int(Y), ldy))
+    return int(_lib.tbg_gemm_grouped_wgrad_workspace_query(groups, M, P, Q, _enum(DTYPES, ab_dtype), X, ldx,
+                                                           Y, ldy))
 
 
 def gemm_grouped_wgrad(groups: int, M: int, P: int, Q: int, offsets: int, alpha: float, X: int, ldx: int, Y: int,
                        ldy: int, ab_dtype, beta: float, C: int, ldc: int, stride_c: int, c_dtype, workspace: int = 0,
                        workspace_bytes: int = 0, stream: Optional[int] = None) -> None:
     """tbg_gemm_grouped_wgrad: C_e = alpha·X_eᵀ·Y_e + beta·C_e over the rows of every group e."""
-    _check(_lib.tbg_gemm_grouped_wgrad(groups, M, P, Q, int(offsets), float(alpha), int(X), ldx, int(Y), ldy,
-                                       _enum(DTYPES, ab_dtype), float(beta), int(C), ldc, stride_c,
-                                       _enum(DTYPES, c_dtype), int(workspace), int(workspace_bytes), stream or None))
+    _check(_lib.tbg_gemm_grouped_wgrad(groups, M, P, Q, offsets, alpha, X, ldx, Y, ldy,
+                                       _enum(DTYPES, ab_dtype), beta, C, ldc, stride_c,
+                                       _enum(DTYPES, c_dtype), workspace, workspace_bytes, stream or None))
 
 
 def mx4_quantize(rows: int, cols: int, X: int, ldx: int, x_dtype, codes: int, ld_codes: int, scales: int,
                  ld_scales: int, stream: Optional[int] = None) -> None:
     """tbg_mx4_quantize: rows of X as microscaled 4-bit codes and scale bytes."""
-    _check(_lib.tbg_mx4_quantize(rows, cols, int(X), ldx, _enum(DTYPES, x_dtype), int(codes), ld_codes, int(scales),
+    _check(_lib.tbg_mx4_quantize(rows, cols, X, ldx, _enum(DTYPES, x_dtype), codes, ld_codes, scales,
                                  ld_scales, stream or None))
 
 
 def mx4_dequantize(rows: int, cols: int, codes: int, ld_codes: int, scales: int, ld_scales: int, X: int, ldx: int,
                    x_dtype, stream: Optional[int] = None) -> None:
     """tbg_mx4_dequantize: the values of microscaled 4-bit rows."""
-    _check(_lib.tbg_mx4_dequantize(rows, cols, int(codes), ld_codes, int(scales), ld_scales, int(X), ldx,
+    _check(_lib.tbg_mx4_dequantize(rows, cols, codes, ld_codes, scales, ld_scales, X, ldx,
                                    _enum(DTYPES, x_dtype), stream or None))
 
 
 def mx4_gemm(M: int, N: int, K: int, alpha: float, A: int, lda: int, A_scales: int, ld_as: int, B: int, ldb: int,
              B_scales: int, ld_bs: int, beta: float, C: int, ldc: int, c_dtype, stream: Optional[int] = None) -> None:
     """tbg_mx4_gemm: C = alpha·A·Bᵀ + beta·C for microscaled 4-bit A (M×K) and B (N×K)."""
-    _check(_lib.tbg_mx4_gemm(M, N, K, float(alpha), int(A), lda, int(A_scales), ld_as, int(B), ldb, int(B_scales),
-                             ld_bs, float(beta), int(C), ldc, _enum(DTYPES, c_dtype), stream or None))
+    _check(_lib.tbg_mx4_gemm(M, N, K, alpha, A, lda, A_scales, ld_as, B, ldb, B_scales,
+                             ld_bs, beta, C, ldc, _enum(DTYPES, c_dtype), stream or None))
 
 
 def mx4_gemm_grouped(groups: int, M: int, N: int, K: int, offsets: int, alpha: float, A: int, lda: int, A_scales: int,
                      ld_as: int, B: int, ldb: int, stride_b: int, B_scales: int, ld_bs: int, stride_bs: int,
                      beta: float, C: int, ldc: int, c_dtype, stream: Optional[int] = None) -> None:
     """tbg_mx4_gemm_grouped: tbg_mx4_gemm for the rows of every group with its own B."""
-    _check(_lib.tbg_mx4_gemm_grouped(groups, M, N, K, int(offsets), float(alpha), int(A), lda, int(A_scales), ld_as,
-                                     int(B), ldb, stride_b, int(B_scales), ld_bs, stride_bs, float(beta), int(C), ldc,
+    _check(_lib.tbg_mx4_gemm_grouped(groups, M, N, K, offsets, alpha, A, lda, A_scales, ld_as,
+                                     B, ldb, stride_b, B_scales, ld_bs, stride_bs, beta, C, ldc,
                                      _enum(DTYPES, c_dtype), stream or None))
 
 

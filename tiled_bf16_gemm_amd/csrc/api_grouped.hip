@@ -129,6 +129,14 @@ int choose_ragged_tile(const TileChoice* t, int n, double groups, double rows, i
 const TileChoice kTiles16[] = {{256, 1.0}, {128, 0.76}, {64, 0.43}};
 const TileChoice kTiles4[] = {{256, 1.0}, {128, 0.7}, {64, 0.4}};
 
+// Tiles of 64 columns that groups of up to 64 rows make.
+double narrow_tiles(double groups, int64_t N) { return groups * (double)((N + 63) / 64); }
+
+// Whether the kernel of few rows (gemm_rows.hpp, with both sides' figures) takes a product.
+bool takes_few_rows(double groups, double rows, int64_t N, int cus) {
+  return rows <= 16 * groups && narrow_tiles(groups, N) < 0.75 * cus;
+}
+
 bool too_many_tiles(int64_t tiles) { return tiles > INT32_MAX - 8; }
 
 }  // namespace
@@ -178,12 +186,13 @@ tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   const Repack rb = plan_repack(B, groups, stride_b, b_rows, b_cols, ldb, nk);
   st = check_workspace(ra.bytes + rb.bytes, workspace, workspace_bytes);
   if (st != TBG_OK) return st;
-  if (too_many_tiles(tbg::ragged_tiles_bound(M, groups, 64) * ((N + 63) / 64)))
+  if (too_many_tiles(tbg::ragged_tiles_bound(M, groups, 16) * ((N + 15) / 16)))
     return fail(TBG_ERR_UNSUPPORTED, "too many tiles for one launch (M=%lld, N=%lld)", (ll)M, (ll)N);
   int cus = 0;
   st = check_device(&cus);
   if (st != TBG_OK) return st;
   const int b = choose_ragged_tile(kTiles16, 3, (double)(groups < M ? groups : M), (double)M, N, cus);
+  const bool few = nk && takes_few_rows((double)(groups < M ? groups : M), (double)M, N, cus);
   hipStream_t s = (hipStream_t)stream;
   uint8_t* const area = tbg::repack_area(workspace, workspace_bytes, ra.bytes + rb.bytes);
   hipError_t e = hipSuccess;
@@ -210,15 +219,23 @@ tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   p.rows = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  p.group_m = 4;
+  p.group_m = 8;
   p.vec_store = tbg::rows_dword_aligned(C, ldc, out_size(c_dtype));
   p.alpha = alpha;
   p.beta = beta;
   p.scaled = scaled ? 1 : 0;
-  tbg::log_choice("grouped gemm groups=%lld M=%lld N=%lld K=%lld B=%s in=%s out=%s: ring %dx%d; repack A %s, B %s",
+  tbg::log_choice("grouped gemm groups=%lld M=%lld N=%lld K=%lld B=%s in=%s out=%s: %s %dx%d; repack A %s, B %s",
                   (ll)groups, (ll)M, (ll)N, (ll)K, nk ? "nk" : "kn", ab_dtype == TBG_F16 ? "f16" : "bf16",
-                  c_dtype == TBG_F32 ? "f32" : "16-bit", b, b, ra.needed ? "yes" : "no", rb.needed ? "yes" : "no");
-  e = tbg::launch_grouped(p, b, b, ab_dtype == TBG_F16, (int)bl, out_code(c_dtype), s);
+                  c_dtype == TBG_F32 ? "f32" : "16-bit", few ? "rows" : "ring", few ? 16 : b, few ? 16 : b,
+                  ra.needed ? "yes" : "no", rb.needed ? "yes" : "no");
+  if (few) {
+    tbg::Mx4GemmParams q;
+    memset(&q, 0, sizeof(q));
+    q.g = p;
+    e = tbg::launch_few_rows(q, ab_dtype == TBG_F16, out_code(c_dtype), s);
+  } else {
+    e = tbg::launch_grouped(p, b, b, ab_dtype == TBG_F16, (int)bl, out_code(c_dtype), s);
+  }
   if (e != hipSuccess) return fail(TBG_ERR_HIP, "grouped gemm launch: %s", hipGetErrorString(e));
   return TBG_OK;
 }
@@ -397,25 +414,36 @@ tbg_status mx4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, const 
   }
   if (groups == 0 || M == 0 || N == 0) return TBG_OK;
   if (!C) return fail(TBG_ERR_INVALID_VALUE, "C is NULL");
-  const int64_t worst = (ragged ? tbg::ragged_tiles_bound(M, groups, 64) : (M + 63) / 64) * ((N + 63) / 64);
+  const int64_t worst = (ragged ? tbg::ragged_tiles_bound(M, groups, 64) : (M + 15) / 16) * ((N + 15) / 16);
   if (too_many_tiles(worst)) return fail(TBG_ERR_UNSUPPORTED, "too many tiles for one launch (M=%lld, N=%lld)", (ll)M, (ll)N);
   int cus = 0;
   st = check_device(&cus);
   if (st != TBG_OK) return st;
-  int b = 0;
-  if (ragged) {
-    b = choose_ragged_tile(kTiles4, 3, (double)(groups < M ? groups : M), (double)M, N, cus);
+  const double active = ragged ? (double)(groups < M ? groups : M) : 1.0;
+  const bool few = takes_few_rows(active, (double)M, N, cus) && (ragged || M <= 16);
+  // Up to 32 rows a group: 32-row tiles, which copy half as many masked rows of A as 64-row ones (40
+  // groups of one or two rows, N = 4096, K = 2048: 34.7 against 40.0 µs).  Two stages instead of four
+  // let more workgroups share a CU, which pays once there are enough of them (the same product
+  // 34.7 against 40.4 µs); few workgroups need the depth (N = 8192, K = 8192, one row: 17.6 against
+  // 10.0 µs).
+  int bm = 0, bn = 0, stages = 2;
+  if ((double)M <= 32 * active) {
+    bm = 32;
+    bn = 64;
+  } else if (ragged) {
+    bm = bn = choose_ragged_tile(kTiles4, 3, active, (double)M, N, cus);
   } else {
     double best = 0;
     for (const TileChoice& t : kTiles4) {
       const int64_t tiles = ((M + t.b - 1) / t.b) * ((N + t.b - 1) / t.b);
       const double cost = (double)((tiles + cus - 1) / cus) * t.b * t.b / t.eff;
-      if (!b || cost < best * 0.999) {
-        b = t.b;
+      if (!bm || cost < best * 0.999) {
+        bm = bn = t.b;
         best = cost;
       }
     }
   }
+  if (bn == 64 && narrow_tiles(active, N) * ((double)M / active > bm ? (double)M / active / bm : 1) < 4 * cus) stages = 4;
   tbg::Mx4GemmParams p;
   memset(&p, 0, sizeof(p));
   p.g.A = (const uint8_t*)A;
@@ -430,7 +458,7 @@ tbg_status mx4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, const 
   p.g.rows = (int)M;
   p.g.N = (int)N;
   p.g.K = (int)K;
-  p.g.group_m = 8;
+  p.g.group_m = ragged ? 8 : 4;
   p.g.vec_store = tbg::rows_dword_aligned(C, ldc, out_size(c_dtype));
   p.g.alpha = alpha;
   p.g.beta = beta;
@@ -440,9 +468,11 @@ tbg_status mx4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, const 
   p.ld_as = ld_as;
   p.ld_bs = ld_bs;
   p.stride_bs = stride_bs;
-  tbg::log_choice("mx4 gemm groups=%lld M=%lld N=%lld K=%lld out=%s: ring %dx%d", (ll)(ragged ? groups : 1), (ll)M,
-                  (ll)N, (ll)K, c_dtype == TBG_F32 ? "f32" : "bf16", b, b);
-  const hipError_t e = tbg::launch_mx4_gemm(p, b, b, c_dtype == TBG_BF16, (hipStream_t)stream);
+  tbg::log_choice("mx4 gemm groups=%lld M=%lld N=%lld K=%lld out=%s: %s %dx%d, %d stages",
+                  (ll)(ragged ? groups : 1), (ll)M, (ll)N, (ll)K, c_dtype == TBG_F32 ? "f32" : "bf16",
+                  few ? "rows" : "ring", few ? 16 : bm, few ? 16 : bn, few ? 1 : stages);
+  const hipError_t e = few ? tbg::launch_few_rows(p, 2, out_code(c_dtype), (hipStream_t)stream)
+                           : tbg::launch_mx4_gemm(p, bm, bn, stages, c_dtype == TBG_BF16, (hipStream_t)stream);
   if (e != hipSuccess) return fail(TBG_ERR_HIP, "mx4 gemm launch: %s", hipGetErrorString(e));
   return TBG_OK;
 }

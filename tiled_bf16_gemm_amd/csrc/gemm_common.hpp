@@ -67,7 +67,7 @@ struct TileCfg {
   // blocks use the compiler's builtin, which also inserts the dependency waits that the
   // short accumulator reuse distance of a small block needs.
   static constexpr bool AsmMfma = Products >= 64;
-  static_assert(BM % 64 == 0 && BN % 64 == 0 && BM <= 256 && BN <= 256, "tile sizes 64, 128, 256");
+  static_assert((BM == 32 || BM % 64 == 0) && BN % 64 == 0 && BM <= 256 && BN <= 256, "tile sizes 64, 128, 256; 32 rows");
 };
 
 // Workgroup id -> (tile row, tile column).  Ids are dealt round-robin to the 8 XCDs; the first

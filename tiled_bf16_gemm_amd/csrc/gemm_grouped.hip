@@ -27,8 +27,11 @@ hipError_t launch_grouped(GroupedParams p, int bm, int bn, int in, int b_layout,
 hipError_t launch_wgrad(GroupedParams p, int bm, int bn, int in, int out, hipStream_t stream) {
   p.tiles_m = (p.M + bm - 1) / bm;
   p.tiles_n = (p.N + bn - 1) / bn;
-  const int64_t grid = (int64_t)p.groups * p.tiles_m * p.tiles_n;
-  if (grid == 0) return hipSuccess;
+  const int64_t per_group = (int64_t)p.tiles_m * p.tiles_n;
+  if (per_group == 0 || p.groups == 0) return hipSuccess;
+  p.per_xcd = per_group > 8 ? (int)(per_group / 8) : 1;
+  p.by_rows = p.groups > 1 && p.groups <= 64 && p.rows >= 256 * p.groups;
+  const int64_t round = 8ll * p.per_xcd, grid = (per_group * p.groups + round - 1) / round * round;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
   if (bm == 256 && bn == 256) return launch_wgrad_tile<256, 2>(p, in, out, (unsigned)grid, stream);
   if (bm == 128 && bn == 128) return launch_wgrad_tile<128, 2>(p, in, out, (unsigned)grid, stream);

@@ -265,13 +265,10 @@ __global__ void __launch_bounds__(kThreads, (RingCfg<BM, BN, S>::MinBlocks)) gem
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RingCfg<BM, BN, S>::LdsBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int tm, tn, begin, end;
-  map_tile(blockIdx.x, gridDim.x, p.groups * p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-  const int g = tm / p.tiles_m;
-  group_rows(p.offsets, g, p.rows, begin, end);
-  begin = __builtin_amdgcn_readfirstlane(begin);
-  end = __builtin_amdgcn_readfirstlane(end);
-  const int m0 = (tm - g * p.tiles_m) * BM, n0 = tn * BN, sum = end - begin;
+  GradTile t;
+  if (!grad_tile(p, blockIdx.x, t)) return;
+  const int g = t.group, begin = t.begin, sum = t.rows;
+  const int m0 = t.tm * BM, n0 = t.tn * BN;
   const TileBox ba = make_box<kSumOuter>(p.A + (int64_t)begin * p.lda + (int64_t)m0 * 2, (uint32_t)p.lda, p.M - m0, sum);
   const TileBox bb = make_box<kSumOuter>(p.B + (int64_t)begin * p.ldb + (int64_t)n0 * 2, (uint32_t)p.ldb, p.N - n0, sum);
   f32x4_t acc[T::FN][T::FM];

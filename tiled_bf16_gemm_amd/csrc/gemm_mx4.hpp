@@ -49,7 +49,8 @@ template <int BM, int BN, int S>
 struct Mx4Cfg {
   using T = TileCfg<BM, BN>;
   static_assert(S % 2 == 0, "a pair of K tiles shares its scale copies");
-  static constexpr int Rows = BM + BN;
+  static constexpr int RowsA = BM < 64 ? 64 : BM;           // an atom's 64 rows are all A's or all B's
+  static constexpr int Rows = RowsA + BN;
   static constexpr int ScaleBytes = Rows * 16;             // scales of one pair of K tiles
   static constexpr int Buffers = S / 2 + 1 <= 2 ? 2 : 4;   // pairs held: the S/2 in flight and the one in use
   static constexpr int ScaleAtoms = Rows < 256 ? 1 : Rows / 256;  // per wave and pair
@@ -89,7 +90,7 @@ template <class C, int S>
 __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uint8_t* smem, const Mx4Box& box,
                                          int wave, int lane) {
   using T = typename C::T;
-  constexpr int FM = T::FM, FN = T::FN, AT = T::AtomsA, BT = T::AtomsB, A = T::Atoms, P = T::Products, R = T::Reads;
+  constexpr int FM = T::FM, AT = T::AtomsA, BT = T::AtomsB, A = T::Atoms, P = T::Products, R = T::Reads;
   constexpr int SA = C::ScaleAtoms;
   const int ktiles = box.blocks > 0 ? (box.blocks + 7) / 8 : 1;
   const int g = lane >> 4;
@@ -110,12 +111,12 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
   // Scales: row `line` of the BM + BN scale rows (A's, then B's), 16 bytes each.
   uint32_t ls[SA];
   const int line0 = 64 * SA * wave;  // this wave's first scale row, uniform: all A's or all B's
-  const bool scales_a = line0 < T::BM, scales_none = line0 >= C::Rows;
+  const bool scales_a = line0 < C::RowsA, scales_none = line0 >= C::Rows;
   const uint32_t pitch_s = scales_a ? box.pitch_as : box.pitch_bs;
 #pragma unroll
   for (int i = 0; i < SA; ++i) {
-    const int row = line0 - (scales_a ? 0 : T::BM) + 64 * i + lane;
-    ls[i] = scales_none || row >= (scales_a ? box.rows_a : box.rows_b) ? kOobOffset : (uint32_t)row * pitch_s;
+    const int row = line0 - (scales_a ? 0 : C::RowsA) + 64 * i + lane;
+    ls[i] = scales_none || row >= (scales_a ? min(box.rows_a, T::BM) : box.rows_b) ? kOobOffset : (uint32_t)row * pitch_s;
   }
   const rsrc_t rs0 = scales_a ? box.ras : box.rbs;
 
@@ -163,7 +164,7 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
   };
   // Scale bytes of fragment i for K tile kt: blocks 2g and 2g+1 of the row.
   const uint8_t* const scales = smem + S * T::StageBytes;
-  const int sa_lane = (wm * T::TM + (lane & 15)) * 16 + 2 * g, sb_lane = (T::BM + wn * T::TN + (lane & 15)) * 16 + 2 * g;
+  const int sa_lane = (wm * T::TM + (lane & 15)) * 16 + 2 * g, sb_lane = (C::RowsA + wn * T::TN + (lane & 15)) * 16 + 2 * g;
   auto read_scale = [&](uint32_t (&s)[R], int kt, int i) __attribute__((always_inline)) {
     const uint8_t* buf = scales + ((kt >> 1) & (C::Buffers - 1)) * C::ScaleBytes + (kt & 1) * 8;
     s[i] = *(const uint16_t*)(buf + (i < FM ? sa_lane + i * 256 : sb_lane + (i - FM) * 256));

@@ -127,6 +127,8 @@ struct GroupedParams {
   int groups, rows;
   int M, N, K;
   int tiles_m, tiles_n, group_m;
+  int per_xcd;     // weight gradient: consecutive tiles of a group per XCD
+  int by_rows;     // weight gradient: the groups run in the order of their rows (at most 64 groups)
   int vec_store;
   float alpha, beta;
   int scaled;
@@ -163,7 +165,11 @@ struct Mx4GemmParams {
   const uint8_t* Bs;
   int64_t ld_as, ld_bs, stride_bs;
 };
-hipError_t launch_mx4_gemm(Mx4GemmParams p, int bm, int bn, int out_bf16, hipStream_t stream);
+// Tiles 256×256 and 128×128 (2 stages), 64×64 and 32×64 (2 or 4 stages).
+hipError_t launch_mx4_gemm(Mx4GemmParams p, int bm, int bn, int stages, int out_bf16, hipStream_t stream);
+// Products with few rows (gemm_rows.hpp), B stored N×K, at most 16 rows when dense; fmt 0 bf16, 1
+// fp16 (A, B and their pitches as GroupedParams), 2 microscaled 4-bit; out as launch_grouped.
+hipError_t launch_few_rows(Mx4GemmParams p, int fmt, int out, hipStream_t stream);
 
 // fp8 GEMM (gemm_fp8.hpp): p in units of two fp8 values (lda, ldb, K, kchunks as for 16-bit data
 // of half the width); fmt 0 E4M3, 1 E5M2; tiles 256×256, 128×128, 64×64.

@@ -14,9 +14,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-namespace tbg {
+#include "launch.hpp"
 
-constexpr int kMaxGroups = 4096;  // 64 per lane
+namespace tbg {
 
 // Rows of group g: begin .. end-1, inside 0 .. rows whatever the offsets hold.
 __device__ __forceinline__ void group_rows(const int32_t* offsets, int g, int rows, int& begin, int& end) {
@@ -36,6 +36,20 @@ __device__ __forceinline__ int wave_prefix_sum(int v) {
   return v;
 }
 
+// Tile `id` of a group's tiles_m × tiles_n: column-major inside bands of tile rows, so that the
+// tiles an XCD computes at one time share operand rows in its L2.  The bands are as near to
+// `height` rows as equal bands can be (a thin last band would read the whole of B once more).
+__device__ __forceinline__ void band_tile(int id, int tiles_m, int tiles_n, int height, int& tm, int& tn) {
+  const int bands = max(1, (tiles_m + height / 2) / height);
+  const int low = tiles_m / bands, more = tiles_m - low * bands;  // the first `more` bands have low + 1 rows
+  const int split = more * (low + 1) * tiles_n;
+  const int h = id < split ? low + 1 : low;
+  const int rest = id < split ? id : id - split;
+  const int band = rest / (h * tiles_n), in = rest - band * h * tiles_n;
+  tm = (id < split ? 0 : more * (low + 1)) + band * h + in % h;
+  tn = in / h;
+}
+
 struct RaggedTile {
   int group;
   int row0;  // first row of the tile
@@ -45,10 +59,10 @@ struct RaggedTile {
 
 // The tile of workgroup `bid`, BM rows high, of `tiles_n` tile columns; false when there is none
 // (the grid is an upper bound).  Workgroups are dealt round-robin to the 8 XCDs, so XCD x gets
-// the x-th eighth of the tiles that exist, in order: groups one after another, and inside a group
-// column-major within `group_m` tile rows, which keeps a group's operands in few L2 caches.
+// the x-th eighth of the tiles that exist, in order: groups one after another, inside a group
+// in band_tile's, which keeps a group's operands in few L2 caches.
 template <int BM>
-__device__ __forceinline__ bool ragged_tile(const int32_t* offsets, int groups, int rows, int tiles_n, int group_m,
+__device__ __forceinline__ bool ragged_tile(const int32_t* offsets, int groups, int rows, int tiles_n, int height,
                                             int bid, RaggedTile& t) {
   const int lane = threadIdx.x & 63;
   const int per = (groups + 63) >> 6, g0 = lane * per;
@@ -84,13 +98,56 @@ __device__ __forceinline__ bool ragged_tile(const int32_t* offsets, int groups, 
   t.group = __builtin_amdgcn_readlane(found, src);
   const int b = __builtin_amdgcn_readlane(fb, src), e = __builtin_amdgcn_readlane(fe, src);
   const int in_group = __builtin_amdgcn_readlane(fi, src);
-  const int tiles_m = (e - b + BM - 1) / BM;
-  const int per_band = group_m * tiles_n;
-  const int band = in_group / per_band, first = band * group_m;
-  const int height = min(tiles_m - first, group_m), in_band = in_group - band * per_band;
-  t.row0 = b + (first + in_band % height) * BM;
+  int tm;
+  band_tile(in_group, (e - b + BM - 1) / BM, tiles_n, height, tm, t.tn);
+  t.row0 = b + tm * BM;
   t.rows = e - t.row0;
-  t.tn = in_band / height;
+  return true;
+}
+
+// The tile of workgroup `bid` of the weight gradient.
+struct GradTile {
+  int group, begin, rows;  // the group and its rows
+  int tm, tn;
+};
+
+// Every group has the same tiles but its own number of rows, and so its own cost per tile.  Each
+// XCD takes an eighth of every group's tiles (p.per_xcd consecutive ones, column-major within
+// bands of tile rows, so that they share operand rows in its L2), so the XCDs stay level however
+// the rows are split; and (p.by_rows, up to 64 groups) they run in the order of their rows, the longest first, so
+// that the last workgroups to start are the short ones.  (One contiguous eighth of all tiles per
+// XCD, as the products of equal tiles use, left the XCD of the longest group running alone: 381 us
+// against PLACEHOLDER us for 8 groups of 16384 rows in all, 4096×2048.)
+__device__ __forceinline__ bool grad_tile(const GroupedParams& p, int bid, GradTile& t) {
+  const int lane = threadIdx.x & 63;
+  const int per_group = p.tiles_m * p.tiles_n;
+  const int x = bid & 7, i = bid >> 3, c = p.per_xcd;
+  const int id = i / c * (8 * c) + x * c + i % c;
+  const int place = id / per_group;
+  if (place >= p.groups) return false;
+  int g = place, begin, end;
+  if (p.by_rows) {
+    int b = 0, e = 0;
+    if (lane < p.groups) group_rows(p.offsets, lane, p.rows, b, e);
+    const int rows = lane < p.groups ? e - b : -1;
+    int rank = 0;  // groups that run before this lane's: more rows, or as many and an earlier number
+    for (int j = 0; j < p.groups; ++j) {
+      const int other = __builtin_amdgcn_readlane(rows, j);
+      rank += other > rows || (other == rows && j < lane);
+    }
+    g = __builtin_ctzll(__ballot(rank == place && lane < p.groups));
+    begin = __builtin_amdgcn_readlane(b, g);
+    end = __builtin_amdgcn_readlane(e, g);
+  } else {
+    group_rows(p.offsets, g, p.rows, begin, end);
+    begin = __builtin_amdgcn_readfirstlane(begin);
+    end = __builtin_amdgcn_readfirstlane(end);
+  }
+  const int in_group = id - place * per_group;
+  band_tile(in_group, p.tiles_m, p.tiles_n, p.group_m, t.tm, t.tn);
+  t.group = g;
+  t.begin = begin;
+  t.rows = end - begin;
   return true;
 }
 

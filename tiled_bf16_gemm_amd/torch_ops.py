@@ -103,29 +103,48 @@ def gemm(A: torch.Tensor, B: torch.Tensor, b_layout: str = "kn", out_dtype: str 
 
 
 # ---- ragged groups and microscaled 4-bit data ------------------------------------------------------
-# These calls run with the operands' device current, on `stream` (default: that device's current
-# stream).  What they allocate belongs to that stream.
 
-def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device != device:
-        raise ValueError(f"stream is on {s.device}, the operands on {device}")
-    return torch.cuda.stream(s), s
+class _Launch:
+    """One call's place: the operands' device current, and what the call allocates on `stream`
+    (default: that device's current stream).  Gives the stream's handle."""
+    __slots__ = ("handle", "ctx")
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        if stream is None:
+            # (the raw handle: building a torch.cuda.Stream object for it costs 1.8 us a call)
+            self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+            self.ctx = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+
+    def __enter__(self) -> int:
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
 
 def _require_offsets(offsets: torch.Tensor, device: torch.device) -> int:
-    if (not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1
-            or not offsets.is_contiguous()):
+    if not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous 1-D int32 CUDA tensor of groups + 1 values")
     if offsets.device != device:
         raise ValueError(f"offsets is on {offsets.device}, A on {device}: every operand must be on one device")
-    return offsets.numel() - 1
+    groups = offsets.shape[0] - 1
+    if groups < 0:
+        raise ValueError("offsets must hold groups + 1 values")
+    return groups
 
 
-def _rows_of(t: torch.Tensor) -> int:
+def _pitch(shape, strides) -> int:
     """Row stride of a matrix, or of each matrix of a stack: a single row's is never used, whatever
     torch says it is."""
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1], 1)
+    return strides[-2] if shape[-2] > 1 else max(strides[-2], shape[-1], 1)
 
 
 def _require_stack(t: torch.Tensor, name: str, device: torch.device):
@@ -137,29 +156,33 @@ def _require_stack(t: torch.Tensor, name: str, device: torch.device):
         raise ValueError(f"{name} is on {t.device}, A on {device}: every operand must be on one device")
 
 
-def _require_out(out: torch.Tensor, shape, dtype: torch.dtype, device: torch.device):
-    if not out.is_cuda or out.device != device or out.dtype != dtype or tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out must be a {tuple(shape)} {dtype} tensor on {device} (got {tuple(out.shape)} {out.dtype} "
-                         f"on {out.device})")
-    if out.stride(-1) != 1 and out.shape[-1] > 1:
-        raise ValueError("out must have a unit inner stride")
-
-
-def _out_type(out_dtype: str, allowed) -> torch.dtype:
+def _output(out: Optional[torch.Tensor], shape, out_dtype: str, allowed, device: torch.device) -> torch.Tensor:
+    """The caller's `out`, checked, or a new tensor."""
     if out_dtype not in allowed:
         raise ValueError(f"out_dtype must be one of {', '.join(allowed)} (got {out_dtype!r})")
-    return _TORCH_OF[out_dtype]
+    dtype = _TORCH_OF[out_dtype]
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.dtype != dtype or tuple(out.shape) != shape or out.device != device:
+        raise ValueError(f"out must be a {shape} {dtype} tensor on {device} (got {tuple(out.shape)} {out.dtype} on "
+                         f"{out.device})")
+    if out.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError("out must have a unit inner stride")
+    return out
 
 
-def _workspace(need: int, workspace: Optional[torch.Tensor], device: torch.device) -> Optional[torch.Tensor]:
-    _require_workspace(workspace, device)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        return torch.empty(2 * need, dtype=torch.uint8, device=device)
-    return workspace
-
-
-def _ptr_bytes(t: Optional[torch.Tensor]):
-    return (0, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+def _workspace(need: int, workspace: Optional[torch.Tensor], device: torch.device):
+    """(address, bytes) of the caller's workspace where it suffices, else of a new one (returned last,
+    to be held until the call is enqueued)."""
+    if workspace is None:
+        if need == 0:
+            return 0, 0, None
+    else:
+        _require_workspace(workspace, device)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        # twice the need: successive calls alternate the halves their repacks land in
+        workspace = torch.empty(2 * need, dtype=torch.uint8, device=device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, b_layout: str = "kn",
@@ -172,30 +195,34 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, b_layo
     Gradients, for dC of C's shape: of the rows gemm_grouped(dC, B, offsets, the other layout), of B
     gemm_grouped_wgrad(A, dC, offsets) for "kn" and gemm_grouped_wgrad(dC, A, offsets) for "nk"."""
     _require(A, "A")
-    _require_stack(B, "B", A.device)
-    groups = _require_offsets(offsets, A.device)
+    device = A.device
+    _require_stack(B, "B", device)
+    groups = _require_offsets(offsets, device)
     ab = _AB_OF.get(A.dtype)
     if ab not in ("bf16", "f16") or B.dtype != A.dtype:
         raise ValueError("A and B must have the same dtype: bfloat16 or float16")
-    if b_layout not in ("kn", "nk"):
-        raise ValueError(f"b_layout must be 'kn' or 'nk' (got {b_layout!r})")
     M, K = A.shape
-    N, Kb = (B.shape[2], B.shape[1]) if b_layout == "kn" else (B.shape[1], B.shape[2])
+    shape_b = B.shape
+    if b_layout == "nk":
+        matrices, N, Kb = shape_b
+    elif b_layout == "kn":
+        matrices, Kb, N = shape_b
+    else:
+        raise ValueError(f"b_layout must be 'kn' or 'nk' (got {b_layout!r})")
     if Kb != K:
         raise ValueError(f"inner sizes differ: {K} vs {Kb}")
-    if B.shape[0] != groups:
-        raise ValueError(f"B holds {B.shape[0]} matrices, offsets {groups} groups")
-    dtype = _out_type(out_dtype, ("f32", ab))
-    ctx, s = _on(A.device, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=A.device)
-        _require_out(out, (M, N), dtype, A.device)
-        lda, ldb, sb = _rows_of(A), _rows_of(B), B.stride(0)
-        need = tbg.gemm_grouped_workspace_query(groups, M, N, K, ab, A.data_ptr(), lda, B.data_ptr(), ldb, sb, b_layout)
-        ws_ptr, ws_bytes = _ptr_bytes(_workspace(need, workspace, A.device))
-        tbg.gemm_grouped(groups, M, N, K, offsets.data_ptr(), alpha, A.data_ptr(), lda, B.data_ptr(), ldb, sb, b_layout,
-                         ab, beta, out.data_ptr(), _rows_of(out), out_dtype, ws_ptr, ws_bytes, int(s.cuda_stream))
+    if matrices != groups:
+        raise ValueError(f"B holds {matrices} matrices, offsets {groups} groups")
+    with _Launch(device, stream) as handle:
+        out = _output(out, (M, N), out_dtype, ("f32", ab), device)
+        a, b, st_b = A.data_ptr(), B.data_ptr(), B.stride()
+        lda, ldb, sb = _pitch((M, K), A.stride()), _pitch(shape_b, st_b), st_b[0]
+        # whole 16-byte rows everywhere need no repack; the query knows the exact rule
+        need = 0 if (lda | ldb | sb | K) % 8 == 0 and (a | b) % 16 == 0 else \
+            tbg.gemm_grouped_workspace_query(groups, M, N, K, ab, a, lda, b, ldb, sb, b_layout)
+        ws_ptr, ws_bytes, held = _workspace(need, workspace, device)
+        tbg.gemm_grouped(groups, M, N, K, offsets.data_ptr(), alpha, a, lda, b, ldb, sb, b_layout, ab, beta,
+                         out.data_ptr(), _pitch((M, N), out.stride()), out_dtype, ws_ptr, ws_bytes, handle)
     return out
 
 
@@ -207,57 +234,60 @@ def gemm_grouped_wgrad(X: torch.Tensor, Y: torch.Tensor, offsets: torch.Tensor, 
     Y: (M, Q), bf16 or fp16; out: (groups, P, Q) of type "f32" or X's.  An empty group's C is
     beta·C (zeros when beta == 0)."""
     _require(X, "X")
-    _require(Y, "Y", X.device)
-    groups = _require_offsets(offsets, X.device)
+    device = X.device
+    _require(Y, "Y", device)
+    groups = _require_offsets(offsets, device)
     ab = _AB_OF.get(X.dtype)
     if ab not in ("bf16", "f16") or Y.dtype != X.dtype:
         raise ValueError("X and Y must have the same dtype: bfloat16 or float16")
-    M, P = X.shape
-    if Y.shape[0] != M:
-        raise ValueError(f"X has {M} rows, Y {Y.shape[0]}")
-    Q = Y.shape[1]
-    dtype = _out_type(out_dtype, ("f32", ab))
-    ctx, s = _on(X.device, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty((groups, P, Q), dtype=dtype, device=X.device)
-        _require_out(out, (groups, P, Q), dtype, X.device)
-        ldx, ldy = _rows_of(X), _rows_of(Y)
-        need = tbg.gemm_grouped_wgrad_workspace_query(groups, M, P, Q, ab, X.data_ptr(), ldx, Y.data_ptr(), ldy)
-        ws_ptr, ws_bytes = _ptr_bytes(_workspace(need, workspace, X.device))
-        tbg.gemm_grouped_wgrad(groups, M, P, Q, offsets.data_ptr(), alpha, X.data_ptr(), ldx, Y.data_ptr(), ldy, ab,
-                               beta, out.data_ptr(), _rows_of(out), out.stride(0), out_dtype, ws_ptr, ws_bytes,
-                               int(s.cuda_stream))
+    (M, P), (My, Q) = X.shape, Y.shape
+    if My != M:
+        raise ValueError(f"X has {M} rows, Y {My}")
+    with _Launch(device, stream) as handle:
+        out = _output(out, (groups, P, Q), out_dtype, ("f32", ab), device)
+        x, y, st_c = X.data_ptr(), Y.data_ptr(), out.stride()
+        ldx, ldy = _pitch((M, P), X.stride()), _pitch((M, Q), Y.stride())
+        need = 0 if (ldx | ldy) % 8 == 0 and (x | y) % 16 == 0 else \
+            tbg.gemm_grouped_wgrad_workspace_query(groups, M, P, Q, ab, x, ldx, y, ldy)
+        ws_ptr, ws_bytes, held = _workspace(need, workspace, device)
+        tbg.gemm_grouped_wgrad(groups, M, P, Q, offsets.data_ptr(), alpha, x, ldx, y, ldy, ab, beta, out.data_ptr(),
+                               _pitch((P, Q), st_c[1:]), st_c[0], out_dtype, ws_ptr, ws_bytes, handle)
     return out
 
 
-def _require_mx4(codes: torch.Tensor, scales: torch.Tensor, name: str, device: Optional[torch.device] = None):
-    for t, what in ((codes, "codes"), (scales, "scales")):
-        if not t.is_cuda or t.dtype != torch.uint8 or t.dim() not in (2, 3):
-            raise ValueError(f"{name}'s {what} must be a 2-D or 3-D uint8 CUDA tensor")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError(f"{name}'s {what} must have a unit inner stride")
-        if t.device != (device if device is not None else codes.device):
-            raise ValueError(f"{name}'s {what} is on {t.device}: every operand must be on one device")
-    if codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != 16 * scales.shape[-1]:
-        raise ValueError(f"{name}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not belong together "
-                         "(16 bytes of codes and one scale per 32 values)")
+def _require_mx4(codes: torch.Tensor, scales: torch.Tensor, name: str, device: torch.device):
+    """Codes and scales that belong together; returns the codes' shape."""
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda:
+        raise ValueError(f"{name}'s codes and scales must be uint8 CUDA tensors")
+    if codes.device != device or scales.device != device:
+        raise ValueError(f"{name} is on {codes.device} and {scales.device}: every operand must be on one device")
+    shape, blocks = codes.shape, scales.shape
+    dims = len(shape)
+    if (dims not in (2, 3) or len(blocks) != dims or shape[0] != blocks[0] or shape[dims - 2] != blocks[dims - 2]
+            or shape[dims - 1] != 16 * blocks[dims - 1]):
+        raise ValueError(f"{name}: codes {tuple(shape)} and scales {tuple(blocks)} do not belong together (matrices or "
+                         "stacks, 16 bytes of codes and one scale per 32 values)")
+    if (codes.stride(-1) != 1 and shape[-1] > 1) or (scales.stride(-1) != 1 and blocks[-1] > 1):
+        raise ValueError(f"{name}'s codes and scales must have a unit inner stride")
+    return shape
 
 
 def _mx4_pitch(t: torch.Tensor) -> int:
     """Row pitch in bytes, of a single row its length rounded up to 16."""
-    return t.stride(-2) if t.shape[-2] > 1 else -(-t.shape[-1] // 16) * 16
+    shape = t.shape
+    return t.stride(-2) if shape[-2] > 1 else -(-shape[-1] // 16) * 16
 
 
 def _flat_rows(t: torch.Tensor, name: str) -> torch.Tensor:
-    """A 2-D view of a matrix or of a stack of matrices whose rows lie at one pitch."""
-    if t.dim() == 3:
-        if t.shape[1] == 1:
-            return t[:, 0]
-        if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) != t.shape[1] * t.stride(1):
-            raise ValueError(f"{name}: the matrices of a stack must follow one another at the rows' pitch")
-        return t.as_strided((t.shape[0] * t.shape[1], t.shape[2]), (t.stride(1), t.stride(2)))
-    return t
+    """A matrix, or the 2-D view of a stack of matrices whose rows lie at one pitch."""
+    if t.dim() == 2:
+        return t
+    n, rows, cols = t.shape
+    if rows == 1:
+        return t[:, 0]
+    if n > 1 and rows > 0 and t.stride(0) != rows * t.stride(1):
+        raise ValueError(f"{name}: the matrices of a stack must follow one another at the rows' pitch")
+    return t.as_strided((n * rows, cols), (t.stride(1), t.stride(2)))
 
 
 def mx4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
@@ -265,25 +295,27 @@ def mx4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: 
     """Rows of x, (rows, cols) or a stack (n, rows, cols) of fp32, bf16 or fp16, as microscaled 4-bit
     data through tbg_mx4_quantize.  Returns (codes, scales), uint8: two codes per byte, one scale per
     32 values, cols rounded up to whole blocks (zeros).  The scales' rows are 16-byte pitched."""
-    if not x.is_cuda or x.dim() not in (2, 3) or x.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+    x_dtype = _X_OF.get(x.dtype)
+    if not x.is_cuda or x.dim() not in (2, 3) or x_dtype is None:
         raise ValueError("x must be a 2-D or 3-D float32, bfloat16 or float16 CUDA tensor")
     if x.stride(-1) != 1 and x.shape[-1] > 1:
         raise ValueError("x must have a unit inner stride")
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales must be given together")
-    blocks = -(-x.shape[-1] // 32)
-    ctx, s = _on(x.device, stream)
-    with ctx:
+    device, lead, cols = x.device, x.shape[:-1], x.shape[-1]
+    blocks = -(-cols // 32)
+    with _Launch(device, stream) as handle:
         if codes is None:
             pitch = -(-blocks // 16) * 16
-            codes = torch.empty((*x.shape[:-1], 16 * blocks), dtype=torch.uint8, device=x.device)
-            scales = torch.empty((*x.shape[:-1], pitch), dtype=torch.uint8, device=x.device)[..., :blocks]
-        _require_mx4(codes, scales, "x", x.device)
-        if tuple(codes.shape) != (*x.shape[:-1], 16 * blocks):
-            raise ValueError(f"codes must be {(*x.shape[:-1], 16 * blocks)} (got {tuple(codes.shape)})")
+            codes = torch.empty((*lead, 16 * blocks), dtype=torch.uint8, device=device)
+            scales = torch.empty((*lead, pitch), dtype=torch.uint8, device=device)
+            if pitch != blocks:
+                scales = scales[..., :blocks]
+        elif _require_mx4(codes, scales, "x", device) != (*lead, 16 * blocks):
+            raise ValueError(f"codes must be {(*lead, 16 * blocks)} (got {tuple(codes.shape)})")
         x2, c2, s2 = _flat_rows(x, "x"), _flat_rows(codes, "codes"), _flat_rows(scales, "scales")
-        tbg.mx4_quantize(x2.shape[0], x2.shape[1], x2.data_ptr(), _rows_of(x2), _X_OF[x.dtype], c2.data_ptr(),
-                         _mx4_pitch(c2), s2.data_ptr(), _mx4_pitch(s2), int(s.cuda_stream))
+        tbg.mx4_quantize(x2.shape[0], cols, x2.data_ptr(), _pitch(x2.shape, x2.stride()), x_dtype, c2.data_ptr(),
+                         _mx4_pitch(c2), s2.data_ptr(), _mx4_pitch(s2), handle)
     return codes, scales
 
 
@@ -291,21 +323,16 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: Optional[int
                    out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The values of mx4_quantize's codes and scales through tbg_mx4_dequantize: the first `cols`
     columns (default: all), of type "f32", "bf16" or "f16"."""
-    _require_mx4(codes, scales, "codes")
-    full = 2 * codes.shape[-1]
-    cols = full if cols is None else int(cols)
-    if not (full - 32 < cols <= full or (cols == 0 and full == 0)):
-        raise ValueError(f"cols must end in the last block of 32: {full - 31}..{full} (got {cols})")
-    dtype = _out_type(out_dtype, ("f32", "bf16", "f16"))
-    ctx, s = _on(codes.device, stream)
-    with ctx:
-        shape = (*codes.shape[:-1], cols)
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=codes.device)
-        _require_out(out, shape, dtype, codes.device)
+    device = codes.device
+    *lead, half = _require_mx4(codes, scales, "codes", device)
+    cols = 2 * half if cols is None else int(cols)
+    if not (2 * half - 32 < cols <= 2 * half):
+        raise ValueError(f"cols must end in the last block of 32: {max(0, 2 * half - 31)}..{2 * half} (got {cols})")
+    with _Launch(device, stream) as handle:
+        out = _output(out, (*lead, cols), out_dtype, ("f32", "bf16", "f16"), device)
         o2, c2, s2 = _flat_rows(out, "out"), _flat_rows(codes, "codes"), _flat_rows(scales, "scales")
         tbg.mx4_dequantize(o2.shape[0], cols, c2.data_ptr(), _mx4_pitch(c2), s2.data_ptr(), _mx4_pitch(s2),
-                           o2.data_ptr(), _rows_of(o2), out_dtype, int(s.cuda_stream))
+                           o2.data_ptr(), _pitch(o2.shape, o2.stride()), out_dtype, handle)
     return out
 
 
@@ -315,22 +342,18 @@ def mx4_gemm(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scales:
     """C = alpha·A·Bᵀ + beta·C for microscaled 4-bit A (M, K/2 codes) and B (N, K/2 codes), each with
     its scales (rows, K/32), through tbg_mx4_gemm.  Codes and scales 16-byte aligned and pitched, as
     mx4_quantize makes them."""
-    _require_mx4(A, a_scales, "A")
-    _require_mx4(B, b_scales, "B", A.device)
-    if A.dim() != 2 or B.dim() != 2:
+    device = A.device
+    shape_a, shape_b = _require_mx4(A, a_scales, "A", device), _require_mx4(B, b_scales, "B", device)
+    if len(shape_a) != 2 or len(shape_b) != 2:
         raise ValueError("A and B must be matrices (mx4_gemm_grouped takes stacks)")
-    if A.shape[1] != B.shape[1]:
-        raise ValueError(f"inner sizes differ: {2 * A.shape[1]} vs {2 * B.shape[1]}")
-    (M, N), K = (A.shape[0], B.shape[0]), 2 * A.shape[1]
-    dtype = _out_type(out_dtype, ("f32", "bf16"))
-    ctx, s = _on(A.device, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=A.device)
-        _require_out(out, (M, N), dtype, A.device)
-        tbg.mx4_gemm(M, N, K, alpha, A.data_ptr(), _mx4_pitch(A), a_scales.data_ptr(), _mx4_pitch(a_scales),
+    (M, half), (N, half_b) = shape_a, shape_b
+    if half != half_b:
+        raise ValueError(f"inner sizes differ: {2 * half} vs {2 * half_b}")
+    with _Launch(device, stream) as handle:
+        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), device)
+        tbg.mx4_gemm(M, N, 2 * half, alpha, A.data_ptr(), _mx4_pitch(A), a_scales.data_ptr(), _mx4_pitch(a_scales),
                      B.data_ptr(), _mx4_pitch(B), b_scales.data_ptr(), _mx4_pitch(b_scales), beta, out.data_ptr(),
-                     _rows_of(out), out_dtype, int(s.cuda_stream))
+                     _pitch((M, N), out.stride()), out_dtype, handle)
     return out
 
 
@@ -340,26 +363,22 @@ def mx4_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b
     """mx4_gemm for the rows of every group (offsets as gemm_grouped) with its own B, (groups, N, K/2
     codes), through tbg_mx4_gemm_grouped.  Rows of no group keep what `out` holds (without `out`:
     undefined)."""
-    _require_mx4(A, a_scales, "A")
-    _require_mx4(B, b_scales, "B", A.device)
-    groups = _require_offsets(offsets, A.device)
-    if A.dim() != 2 or B.dim() != 3:
+    device = A.device
+    shape_a, shape_b = _require_mx4(A, a_scales, "A", device), _require_mx4(B, b_scales, "B", device)
+    groups = _require_offsets(offsets, device)
+    if len(shape_a) != 2 or len(shape_b) != 3:
         raise ValueError("A must be a matrix and B a stack of matrices")
-    if A.shape[1] != B.shape[2]:
-        raise ValueError(f"inner sizes differ: {2 * A.shape[1]} vs {2 * B.shape[2]}")
-    if B.shape[0] != groups:
-        raise ValueError(f"B holds {B.shape[0]} matrices, offsets {groups} groups")
-    (M, N), K = (A.shape[0], B.shape[1]), 2 * A.shape[1]
-    dtype = _out_type(out_dtype, ("f32", "bf16"))
-    ctx, s = _on(A.device, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=A.device)
-        _require_out(out, (M, N), dtype, A.device)
-        tbg.mx4_gemm_grouped(groups, M, N, K, offsets.data_ptr(), alpha, A.data_ptr(), _mx4_pitch(A),
+    (M, half), (matrices, N, half_b) = shape_a, shape_b
+    if half != half_b:
+        raise ValueError(f"inner sizes differ: {2 * half} vs {2 * half_b}")
+    if matrices != groups:
+        raise ValueError(f"B holds {matrices} matrices, offsets {groups} groups")
+    with _Launch(device, stream) as handle:
+        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), device)
+        tbg.mx4_gemm_grouped(groups, M, N, 2 * half, offsets.data_ptr(), alpha, A.data_ptr(), _mx4_pitch(A),
                              a_scales.data_ptr(), _mx4_pitch(a_scales), B.data_ptr(), _mx4_pitch(B), B.stride(0),
                              b_scales.data_ptr(), _mx4_pitch(b_scales), b_scales.stride(0), beta, out.data_ptr(),
-                             _rows_of(out), out_dtype, int(s.cuda_stream))
+                             _pitch((M, N), out.stride()), out_dtype, handle)
     return out
 
 
