@@ -1,6 +1,7 @@
 // The C ABI of the ragged and the 4-bit products (include/tbg.h): argument checks, repacking and the
 // choice of a tile.  Host code only; kernels are enqueued on the caller's stream.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -102,32 +103,48 @@ tbg_status check_workspace(size_t need, const void* workspace, size_t have) {
 }
 
 // ---- the choice of a tile -------------------------------------------------------------------
-// As the dense products: tiles of the busiest compute unit times a tile's work over its efficiency.
-// How the rows split is not known here; groups of the average size, each ending half way into
-// its last tile, are assumed.
-struct TileChoice {
-  int b;
-  double eff;
+// A round of tiles, one on every slot the chip has for them, takes about `fixed` µs to start and to
+// store and `per` µs for each K tile (128 bytes of a row); the smaller tiles share a CU, and a
+// round that does not fill costs them only `part` of one, since the next tiles start as others end.
+// Measured on MI355X over 8 to 64 groups, K of 300 to 4096 (µs, chosen first): 8 groups of 2048
+// rows, N = 1024, K = 512 26 (128) against 36 (256); 8 of 1024 rows, N = 1024, K = 4096 73 (256)
+// against 91 (128); 100 of 30 rows, N = 700, K = 600 55 (64) against 59 (128).
+struct TileTime {
+  int b, per_cu;
+  double fixed, per, part;
 };
+const TileTime kTiles16[] = {{256, 1, 6.5, 1.25, 1.0}, {128, 2, 5.0, 1.05, 0.25}, {64, 3, 4.0, 0.75, 0.2}};
+const TileTime kTiles4[] = {{256, 1, 6.5, 1.7, 1.0}, {128, 2, 5.0, 1.2, 0.25}, {64, 2, 4.0, 0.37, 0.2}};
 
-int choose_ragged_tile(const TileChoice* t, int n, double groups, double rows, int64_t N, int cus) {
-  int best = 0;
-  double best_cost = 0;
-  for (int i = 0; i < n; ++i) {
-    const double per = rows / groups / t[i].b + 0.5;
-    const double tiles = groups * (per > 1 ? per : 1) * (double)((N + t[i].b - 1) / t[i].b);
-    const double rounds = tiles <= cus ? 1 : tiles / cus;
-    const double cost = rounds * t[i].b * t[i].b / t[i].eff;
-    if (!best || cost < best_cost * 0.999) {
-      best = t[i].b;
-      best_cost = cost;
+double tile_time(const TileTime& t, double tiles, double ktiles, int cus) {
+  double rounds = tiles / ((double)t.per_cu * cus);
+  if (rounds <= 1) rounds = 1;
+  else if (t.part == 1.0) rounds = ceil(rounds);
+  else rounds += t.part;
+  return rounds * (t.fixed + t.per * ktiles);
+}
+
+// The tile for `groups` groups that share `rows` rows.  How the rows split is not known here:
+// groups of the average size are assumed, each ending half way into its last tile.  Up to 64 (160)
+// rows a group the product is bound by the bytes of B, which a tile of 64 (128) rows reads as
+// well with less of it masked (64 groups, N = K = 2048: 64 rows 130 µs with 64-row tiles, 153 with
+// 128; 128 rows 159 µs with 128, 182 with 256).
+int choose_rows_tile(const TileTime (&t)[3], double groups, double rows, int64_t N, double ktiles, int cus) {
+  const double average = rows / groups;
+  int best = 64;
+  double best_time = 0;
+  for (const TileTime& c : t) {
+    if ((c.b > 64 && average <= 64) || (c.b > 128 && average <= 160)) continue;
+    const double per = groups > 1 ? average / c.b + 0.5 : ceil(average / c.b);
+    const double tiles = groups * (per > 1 ? per : 1) * (double)((N + c.b - 1) / c.b);
+    const double time = tile_time(c, tiles, ktiles, cus);
+    if (best_time == 0 || time < best_time) {
+      best = c.b;
+      best_time = time;
     }
   }
   return best;
 }
-
-const TileChoice kTiles16[] = {{256, 1.0}, {128, 0.76}, {64, 0.43}};
-const TileChoice kTiles4[] = {{256, 1.0}, {128, 0.7}, {64, 0.4}};
 
 // Tiles of 64 columns that groups of up to 64 rows make.
 double narrow_tiles(double groups, int64_t N) { return groups * (double)((N + 63) / 64); }
@@ -191,8 +208,9 @@ tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   int cus = 0;
   st = check_device(&cus);
   if (st != TBG_OK) return st;
-  const int b = choose_ragged_tile(kTiles16, 3, (double)(groups < M ? groups : M), (double)M, N, cus);
-  const bool few = nk && takes_few_rows((double)(groups < M ? groups : M), (double)M, N, cus);
+  const double active = (double)(groups < M ? groups : M);
+  const int b = choose_rows_tile(kTiles16, active, (double)M, N, ceil(K / 64.0), cus);
+  const bool few = nk && takes_few_rows(active, (double)M, N, cus);
   hipStream_t s = (hipStream_t)stream;
   uint8_t* const area = tbg::repack_area(workspace, workspace_bytes, ra.bytes + rb.bytes);
   hipError_t e = hipSuccess;
@@ -280,16 +298,15 @@ tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t 
   int cus = 0;
   st = check_device(&cus);
   if (st != TBG_OK) return st;
+  // Every group has the same tiles, its rows are the sum's terms.
   int b = 0;
-  {
-    double best = 0;
-    for (const TileChoice& t : kTiles16) {
-      const int64_t tiles = groups * ((P + t.b - 1) / t.b) * ((Q + t.b - 1) / t.b);
-      const double cost = (double)((tiles + cus - 1) / cus) * t.b * t.b / t.eff;
-      if (!b || cost < best * 0.999) {
-        b = t.b;
-        best = cost;
-      }
+  double best = 0;
+  for (const TileTime& t : kTiles16) {
+    const double tiles = (double)groups * (double)((P + t.b - 1) / t.b) * (double)((Q + t.b - 1) / t.b);
+    const double time = tile_time(t, tiles, ceil((double)M / (double)groups / 64), cus);
+    if (!b || time < best) {
+      b = t.b;
+      best = time;
     }
   }
   hipStream_t s = (hipStream_t)stream;
@@ -430,18 +447,8 @@ tbg_status mx4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, const 
   if ((double)M <= 32 * active) {
     bm = 32;
     bn = 64;
-  } else if (ragged) {
-    bm = bn = choose_ragged_tile(kTiles4, 3, active, (double)M, N, cus);
   } else {
-    double best = 0;
-    for (const TileChoice& t : kTiles4) {
-      const int64_t tiles = ((M + t.b - 1) / t.b) * ((N + t.b - 1) / t.b);
-      const double cost = (double)((tiles + cus - 1) / cus) * t.b * t.b / t.eff;
-      if (!bm || cost < best * 0.999) {
-        bm = bn = t.b;
-        best = cost;
-      }
-    }
+    bm = bn = choose_rows_tile(kTiles4, active, (double)M, N, ceil(K / 256.0), cus);
   }
   if (bn == 64 && narrow_tiles(active, N) * ((double)M / active > bm ? (double)M / active / bm : 1) < 4 * cus) stages = 4;
   tbg::Mx4GemmParams p;

@@ -5,10 +5,13 @@
 // A K tile is 256 values, 128 bytes of codes per row: in bytes the ring, its copy atoms, LDS
 // layout, fragment reads and epilogue are those of the 16-bit kernels (gemm_ring.hpp), and a
 // k-step of 64 bytes is one 16×16×128 product per fragment pair.  Two things are new.
-//  * Scales.  A K tile has 8 scale bytes per row.  They reach LDS as 16-byte chunks, 16 blocks,
-//    of a row: one copy for two K tiles, 64 rows per atom (256×256: two atoms per wave and pair
-//    of tiles, next to 32 atoms of codes).  The instruction takes a lane's scale from one byte of
-//    a register, chosen by an immediate.
+//  * Scales.  A K tile has 8 scale bytes per row.  They reach LDS as the 32 bytes of four K tiles (a
+//    quad), 32 rows per copy atom, two buffers of 32 bytes a row (256×256: 4 atoms per wave and
+//    quad next to 64 atoms of codes; the ring and the buffers are the whole 160 KiB of LDS).  Copies
+//    of 16 bytes per row, for two K tiles, took as many atoms but twice the cache lines (8192³
+//    241 against 234 µs, 2048³ 11.4 against 11.0).  Both 16-byte halves of rows 8..15 of 16 are exchanged in LDS, so that a
+//    fragment's 16 rows, 32 bytes apart, are read from distinct banks.  The instruction takes a lane's
+//    scale from one byte of a register, chosen by an immediate.
 //  * Placement.  Lane l multiplies row l%16 and, in k-step kk, block 2(l/16)+kk of the tile (not
 //    4kk + l/16): its two k-steps then need two neighbouring scale bytes, one 16-bit LDS read per
 //    fragment and K tile.  The sum runs over the tile's blocks in another order, the same for A
@@ -48,20 +51,17 @@ __device__ __forceinline__ void mfma_mx4(f32x4_t& acc, const i32x4_t& a, const i
 template <int BM, int BN, int S>
 struct Mx4Cfg {
   using T = TileCfg<BM, BN>;
-  static_assert(S % 2 == 0, "a pair of K tiles shares its scale copies");
-  static constexpr int RowsA = BM < 64 ? 64 : BM;           // an atom's 64 rows are all A's or all B's
-  static constexpr int Rows = RowsA + BN;
-  static constexpr int ScaleBytes = Rows * 16;             // scales of one pair of K tiles
-  static constexpr int Buffers = S / 2 + 1 <= 2 ? 2 : 4;   // pairs held: the S/2 in flight and the one in use
-  static constexpr int ScaleAtoms = Rows < 256 ? 1 : Rows / 256;  // per wave and pair
-  // Fewer than 256 rows leave waves without scale rows; they copy zeros into a spare area, so
-  // that every wave counts the same copies.
-  static constexpr int SpareBytes = Rows < 256 ? 2048 : 0;
-  static constexpr int ScaleArea = Buffers * ScaleBytes + SpareBytes;
-  static constexpr int LdsBytes = S * T::StageBytes + ScaleArea;
-  static constexpr int MinBlocks = 2 * LdsBytes <= 160 * 1024 ? 2 : 1;
+  static_assert(S == 2 || S == 4, "stages divide the four K tiles of a quad");
+  static constexpr int Rows = BM + BN;
+  static constexpr int QuadBytes = Rows * 32;              // scales of four K tiles
+  static constexpr int ScaleAtoms = (Rows / 32 + 3) / 4;   // per wave and quad (32×64: the last wave has none)
+  static constexpr int RowsWave = 32 * ScaleAtoms;         // each wave's are all A's or all B's
+  static constexpr int LdsBytes = S * T::StageBytes + 2 * QuadBytes;
+  // Workgroups per CU, as many as LDS holds (it is given out in pieces of 1280 bytes).
+  static constexpr int MinBlocks = 128 / ((LdsBytes + 1279) / 1280);
+  static_assert(BM % RowsWave == 0, "whole waves of A's rows");
   static_assert(LdsBytes <= 160 * 1024, "the ring must fit in LDS");
-  static_assert((S - 1) * T::Atoms + S / 2 * ScaleAtoms <= 63, "copies in flight must fit the vmcnt counter");
+  static_assert((S - 1) * T::Atoms + ScaleAtoms <= 63, "copies in flight must fit the vmcnt counter");
 };
 
 // The operands of one workgroup tile: code and scale buffers from the tile's first row, rows that
@@ -82,10 +82,11 @@ struct Mx4Frags {
   i32x4_t a[8], b[8];
 };
 
-// acc += A·Bᵀ over one workgroup tile.  Schedule of the barrier ring; the copies of an even K tile
-// bring the scales of its pair along, and k-step 1 reads the next tile's scales next to its first
-// fragments.  Copies in flight behind the awaited tile: T·(S-2) code atoms and, as S is even, the
-// scales of (S-2)/2 pairs.
+// acc += A·Bᵀ over one workgroup tile.  Schedule of the barrier ring, four K tiles (a quad) per
+// iteration; the first two tiles of a quad bring the next quad's scales along, half each, and
+// k-step 1 reads the next tile's scales next to its first fragments.  A barrier lets the code atoms
+// of the S-2 tiles behind the awaited one be in flight; scale atoms among them (a wave's own number)
+// only make it wait for a few more copies than it needs.
 template <class C, int S>
 __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uint8_t* smem, const Mx4Box& box,
                                          int wave, int lane) {
@@ -108,20 +109,21 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
   for (int i = 0; i < AT; ++i) code_lanes(la[i], 8 * (AT * wave + i), box.pitch_a, box.rows_a);
 #pragma unroll
   for (int i = 0; i < BT; ++i) code_lanes(lb[i], 8 * (BT * wave + i), box.pitch_b, box.rows_b);
-  // Scales: row `line` of the BM + BN scale rows (A's, then B's), 16 bytes each.
+  // Scales: two lanes per row, the halves exchanged in rows 8..15 of 16.
   uint32_t ls[SA];
-  const int line0 = 64 * SA * wave;  // this wave's first scale row, uniform: all A's or all B's
-  const bool scales_a = line0 < C::RowsA, scales_none = line0 >= C::Rows;
+  const int line0 = C::RowsWave * wave;  // this wave's first scale row: all A's or all B's
+  const bool scales_a = line0 < T::BM, has_scales = line0 < C::Rows;
   const uint32_t pitch_s = scales_a ? box.pitch_as : box.pitch_bs;
 #pragma unroll
   for (int i = 0; i < SA; ++i) {
-    const int row = line0 - (scales_a ? 0 : C::RowsA) + 64 * i + lane;
-    ls[i] = scales_none || row >= (scales_a ? min(box.rows_a, T::BM) : box.rows_b) ? kOobOffset : (uint32_t)row * pitch_s;
+    const int row = line0 - (scales_a ? 0 : T::BM) + 32 * i + (lane >> 1);
+    const uint32_t half = (uint32_t)((lane & 1) ^ ((lane >> 4) & 1));
+    ls[i] = row >= (scales_a ? box.rows_a : box.rows_b) ? kOobOffset : (uint32_t)row * pitch_s + half * 16u;
   }
   const rsrc_t rs0 = scales_a ? box.ras : box.rbs;
 
   const uint32_t smem_addr = lds_addr_of(smem);
-  const uint32_t scale_addr = smem_addr + S * T::StageBytes;
+  const uint32_t scale_addr = smem_addr + S * T::StageBytes + line0 * 32;
   struct Copy {
     rsrc_t ra, rb, rs;
     uint32_t lds_a, lds_b, lds_s;
@@ -136,14 +138,15 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
     c.valid = box.blocks - kt * 8;
     c.lds_a = smem_addr + stage * T::StageBytes + AT * wave * 1024;
     c.lds_b = smem_addr + stage * T::StageBytes + T::ABytes + BT * wave * 1024;
-    const int pair = kt >> 1;
-    c.rs = rsrc_advance(rs0, (uint64_t)pair * 16u);
-    c.rs.z = max(rs0.z - pair * 16, 0);
-    c.live_s = pair * 16 < box.blocks;
-    c.lds_s = scale_addr + (scales_none ? C::Buffers * C::ScaleBytes + (wave & 1) * 1024
-                                        : (pair & (C::Buffers - 1)) * C::ScaleBytes + line0 * 16);
     return c;
   };
+  auto scale_copy = [&](Copy& c, int quad) __attribute__((always_inline)) {
+    c.rs = rsrc_advance(rs0, (uint64_t)quad * 32u);
+    c.rs.z = max(rs0.z - quad * 32, 0);
+    c.live_s = quad * 32 < box.blocks;
+    c.lds_s = scale_addr + (quad & 1) * C::QuadBytes;
+  };
+  // atoms 0..A-1: codes; A + i: scale atom i
   auto atom = [&](const Copy& c, int j, auto interior) __attribute__((always_inline)) {
     constexpr bool in = decltype(interior)::value;
     if (j < AT) {
@@ -151,7 +154,7 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
     } else if (j < A) {
       const int i = j - AT;
       issue_atom_if(c.rb, c.lds_b, i * 1024, lb[i].offset, in || lb[i & 1].chunk < c.valid);
-    } else {
+    } else if (C::RowsWave * 4 == C::Rows || has_scales) {
       issue_atom_if(c.rs, c.lds_s, (j - A) * 1024, ls[j - A], in || c.live_s);
     }
   };
@@ -162,12 +165,13 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
     if (i < FM) f.a[i] = *(const i32x4_t*)(s + fa.a_lane + i * 2048 + fa.a_col[kk]);
     else f.b[i - FM] = *(const i32x4_t*)(s + T::ABytes + fa.b_lane + (i - FM) * 2048 + fa.b_col[kk]);
   };
-  // Scale bytes of fragment i for K tile kt: blocks 2g and 2g+1 of the row.
+  // Scale bytes of fragment i for K tile `quad`, QT (0..3): blocks 2g and 2g+1 of the row.
   const uint8_t* const scales = smem + S * T::StageBytes;
-  const int sa_lane = (wm * T::TM + (lane & 15)) * 16 + 2 * g, sb_lane = (C::RowsA + wn * T::TN + (lane & 15)) * 16 + 2 * g;
-  auto read_scale = [&](uint32_t (&s)[R], int kt, int i) __attribute__((always_inline)) {
-    const uint8_t* buf = scales + ((kt >> 1) & (C::Buffers - 1)) * C::ScaleBytes + (kt & 1) * 8;
-    s[i] = *(const uint16_t*)(buf + (i < FM ? sa_lane + i * 256 : sb_lane + (i - FM) * 256));
+  const int lane_s = (lane & 15) * 32 + 2 * g, swap = (lane >> 3) & 1;
+  auto read_scale = [&](uint32_t (&s)[R], int quad, auto qt, int i) __attribute__((always_inline)) {
+    constexpr int QT = decltype(qt)::value;
+    const uint8_t* buf = scales + (quad & 1) * C::QuadBytes + lane_s + ((QT >> 1) ^ swap) * 16 + (QT & 1) * 8;
+    s[i] = *(const uint16_t*)(buf + (i < FM ? wm * T::TM * 32 + i * 512 : (T::BM + wn * T::TN) * 32 + (i - FM) * 512));
   };
   // Zero the bytes of blocks past the end.  The empty statement keeps the masking next to the
   // reads: products written as assembly must not follow a vector instruction that writes their
@@ -182,73 +186,83 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
     }
   };
 
-  // KK: which k-step the products are; the fragments of the other are read meanwhile.
+  // One k-step: KK says which blocks the products take; the fragments of the other k-step are
+  // read meanwhile, and with KK = 1 the scales of K tile `next` (QN of its quad), the code atoms
+  // of `c` and its scale atoms S0 .. S0+NS-1 go out.
   auto step = [&](const Mx4Frags& cur, Mx4Frags& nxt, const uint32_t (&s)[R], uint32_t (&s_nxt)[R], const uint8_t* from,
-                  auto kk, const Copy& c, auto scale_copy, int next_kt, auto interior) __attribute__((always_inline)) {
-    constexpr int KK = decltype(kk)::value;
-    constexpr int NA = KK == 1 ? A + (decltype(scale_copy)::value ? SA : 0) : 0;
+                  auto kk, const Copy& c, auto s0, auto ns, int next, auto qn,
+                  auto interior) __attribute__((always_inline)) {
+    constexpr int KK = decltype(kk)::value, S0 = decltype(s0)::value;
+    constexpr int NA = KK == 1 ? A + decltype(ns)::value : 0;
+    constexpr int H = P / (2 * (NA > 0 ? NA : 1));
+    auto go = [&](int j) __attribute__((always_inline)) { atom(c, j < A ? j : j + S0, interior); };
 #pragma unroll
     for (int i = 0; i < P; ++i) {
 #pragma unroll
       for (int r = (i * R + P - 1) / P; r < ((i + 1) * R + P - 1) / P; ++r) {
         read(nxt, from, 1 - KK, r);
-        if (KK == 1) read_scale(s_nxt, next_kt, r);
+        if (KK == 1) read_scale(s_nxt, next >> 2, qn, r);
       }
-      if (NA > 0) {
-        constexpr int H = P / (2 * (NA > 0 ? NA : 1));
-        if (i >= H) {
+      if (NA > 0 && i >= H) {
 #pragma unroll
-          for (int j = ((i - H) * NA + P - 1) / P; j < ((i + 1 - H) * NA + P - 1) / P; ++j) atom(c, j, interior);
-        }
+        for (int j = ((i - H) * NA + P - 1) / P; j < ((i + 1 - H) * NA + P - 1) / P; ++j) go(j);
       }
       const int fn = i / FM, fm = (fn & 1) ? FM - 1 - i % FM : i % FM;
       mfma_mx4<T::AsmMfma, KK>(acc[fn][fm], cur.b[fn], cur.a[fm], s[FM + fn], s[fm]);
     }
     if (NA > 0) {
-      constexpr int H = P / (2 * (NA > 0 ? NA : 1));
 #pragma unroll
-      for (int j = ((P - H) * NA + P - 1) / P; j < NA; ++j) atom(c, j, interior);
+      for (int j = ((P - H) * NA + P - 1) / P; j < NA; ++j) go(j);
     }
-    if (KK == 1 && !decltype(interior)::value) mask_scales(s_nxt, next_kt);
+    if (KK == 1 && !decltype(interior)::value) mask_scales(s_nxt, next);
   };
 
   Mx4Frags f0, f1;
   uint32_t s0[R], s1[R];
+  {
+    Copy c = make_copy(0, 0);
+    scale_copy(c, 0);
+#pragma unroll
+    for (int j = A; j < A + SA; ++j) atom(c, j, std::false_type{});
+  }
 #pragma unroll
   for (int t = 0; t < S; ++t) {
     const Copy c = make_copy(t, t);
-    if (t % 2 == 0) {
-#pragma unroll
-      for (int j = A; j < A + SA; ++j) atom(c, j, std::false_type{});
-    }
 #pragma unroll
     for (int j = 0; j < A; ++j) atom(c, j, std::false_type{});
   }
-  stage_barrier<A*(S - 1) + SA*(S / 2 - 1)>();  // tile 0 and its pair's scales landed
+  stage_barrier<A*(S - 1)>();  // the first quad's scales and tile 0 landed
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     read(f0, smem, 0, r);
-    read_scale(s0, 0, r);
+    read_scale(s0, 0, std::integral_constant<int, 0>{}, r);
   }
   mask_scales(s0, 0);
   typedef std::integral_constant<int, 0> K0;
   typedef std::integral_constant<int, 1> K1;
-  auto tile = [&](int kt, auto stage, auto interior) __attribute__((always_inline)) {
-    constexpr int cur = decltype(stage)::value, nxt = cur + 1 == S ? 0 : cur + 1;
-    typedef std::integral_constant<bool, cur % 2 == 0> Even;
-    uint32_t (&s)[R] = cur % 2 == 0 ? s0 : s1;
-    uint32_t (&sn)[R] = cur % 2 == 0 ? s1 : s0;
-    step(f0, f1, s, sn, smem + cur * T::StageBytes, K0{}, Copy{}, Even{}, kt + 1, interior);
-    stage_barrier<A*(S - 2) + SA*(S / 2 - 1)>();  // tile kt+1 (and its scales) landed, stage `cur` free
-    step(f1, f0, s, sn, smem + nxt * T::StageBytes, K1{}, make_copy(kt + S, cur), Even{}, kt + 1, interior);
+  // K tile kt, the q-th of its quad (kt - q is a multiple of 4), in stage q % S.
+  auto tile = [&](int kt, auto q, auto interior) __attribute__((always_inline)) {
+    constexpr int Q = decltype(q)::value, cur = Q % S, nxt = (Q + 1) % S;
+    // the next quad's scale atoms: the first half (rounded up) with tile 0, the others with tile 1
+    constexpr int First = (SA + 1) / 2, S0 = Q == 1 ? First : 0, NS = Q == 0 ? First : Q == 1 ? SA - First : 0;
+    typedef std::integral_constant<int, S0> Begin;
+    typedef std::integral_constant<int, NS> Count;
+    typedef std::integral_constant<int, (Q + 1) % 4> Next;
+    uint32_t (&s)[R] = Q % 2 == 0 ? s0 : s1;
+    uint32_t (&sn)[R] = Q % 2 == 0 ? s1 : s0;
+    step(f0, f1, s, sn, smem + cur * T::StageBytes, K0{}, Copy{}, Begin{}, Count{}, kt + 1, Next{}, interior);
+    stage_barrier<A*(S - 2)>();  // tile kt+1 (and its scales) landed, stage `cur` free
+    Copy c = make_copy(kt + S, cur);
+    if (NS > 0) scale_copy(c, (kt >> 2) + 1);
+    step(f1, f0, s, sn, smem + nxt * T::StageBytes, K1{}, c, Begin{}, Count{}, kt + 1, Next{}, interior);
   };
   int kt = 0;
-  for (; kt + 2 * S < ktiles; kt += S)
-    for_stages<S>([&](auto st) __attribute__((always_inline)) { tile(kt + decltype(st)::value, st, std::true_type{}); });
-  for (; kt + S <= ktiles; kt += S)
-    for_stages<S>([&](auto st) __attribute__((always_inline)) { tile(kt + decltype(st)::value, st, std::false_type{}); });
-  for_stages<S - 1>([&](auto st) __attribute__((always_inline)) {
-    if (kt + decltype(st)::value < ktiles) tile(kt + decltype(st)::value, st, std::false_type{});
+  for (; kt + 4 + S < ktiles; kt += 4)
+    for_stages<4>([&](auto q) __attribute__((always_inline)) { tile(kt + decltype(q)::value, q, std::true_type{}); });
+  for (; kt + 4 <= ktiles; kt += 4)
+    for_stages<4>([&](auto q) __attribute__((always_inline)) { tile(kt + decltype(q)::value, q, std::false_type{}); });
+  for_stages<3>([&](auto q) __attribute__((always_inline)) {
+    if (kt + decltype(q)::value < ktiles) tile(kt + decltype(q)::value, q, std::false_type{});
   });
   drain_acc<T>(acc);
   stage_barrier<0>();

@@ -104,19 +104,21 @@ def gemm(A: torch.Tensor, B: torch.Tensor, b_layout: str = "kn", out_dtype: str 
 
 # ---- ragged groups and microscaled 4-bit data ------------------------------------------------------
 
+# These calls check a tensor's place by its device number (get_device(), -1 on the host).
+
 class _Launch:
-    """One call's place: the operands' device current, and what the call allocates on `stream`
+    """One call's place: device number `index` current, and what the call allocates on `stream`
     (default: that device's current stream).  Gives the stream's handle."""
     __slots__ = ("handle", "ctx")
 
-    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
         if stream is None:
             # (the raw handle: building a torch.cuda.Stream object for it costs 1.8 us a call)
-            self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+            self.ctx = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+            self.handle = torch._C._cuda_getCurrentRawStream(index)
         else:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+            if stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, the operands on cuda:{index}")
             self.ctx = torch.cuda.stream(stream)
             self.handle = stream.cuda_stream
 
@@ -130,15 +132,22 @@ class _Launch:
             self.ctx.__exit__(*exc)
 
 
-def _require_offsets(offsets: torch.Tensor, device: torch.device) -> int:
-    if not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
+def _require_offsets(offsets: torch.Tensor, index: int) -> int:
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.shape[0] < 1:
         raise ValueError("offsets must be a contiguous 1-D int32 CUDA tensor of groups + 1 values")
-    if offsets.device != device:
-        raise ValueError(f"offsets is on {offsets.device}, A on {device}: every operand must be on one device")
-    groups = offsets.shape[0] - 1
-    if groups < 0:
-        raise ValueError("offsets must hold groups + 1 values")
-    return groups
+    if offsets.get_device() != index:
+        raise ValueError(f"offsets is on {offsets.device}, the operands on cuda:{index}")
+    return offsets.shape[0] - 1
+
+
+def _require_rows(t: torch.Tensor, name: str, index: int, dims: int = 2):
+    """A row-major matrix (dims 2) or stack of matrices (3) on device `index`; its shape and strides."""
+    shape, strides = t.shape, t.stride()
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} is on {t.device}: every operand must be on one CUDA (HIP) device")
+    if len(shape) != dims or (strides[-1] != 1 and shape[-1] > 1):
+        raise ValueError(f"{name} must be a {dims}-D row-major view (unit inner stride)")
+    return shape, strides
 
 
 def _pitch(shape, strides) -> int:
@@ -147,24 +156,15 @@ def _pitch(shape, strides) -> int:
     return strides[-2] if shape[-2] > 1 else max(strides[-2], shape[-1], 1)
 
 
-def _require_stack(t: torch.Tensor, name: str, device: torch.device):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name} must be a 3-D stack of row-major matrices (unit inner stride)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, A on {device}: every operand must be on one device")
-
-
-def _output(out: Optional[torch.Tensor], shape, out_dtype: str, allowed, device: torch.device) -> torch.Tensor:
+def _output(out: Optional[torch.Tensor], shape, out_dtype: str, allowed, index: int) -> torch.Tensor:
     """The caller's `out`, checked, or a new tensor."""
     if out_dtype not in allowed:
         raise ValueError(f"out_dtype must be one of {', '.join(allowed)} (got {out_dtype!r})")
     dtype = _TORCH_OF[out_dtype]
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if out.dtype != dtype or tuple(out.shape) != shape or out.device != device:
-        raise ValueError(f"out must be a {shape} {dtype} tensor on {device} (got {tuple(out.shape)} {out.dtype} on "
+        return torch.empty(shape, dtype=dtype, device=index)
+    if out.dtype != dtype or tuple(out.shape) != shape or out.get_device() != index:
+        raise ValueError(f"out must be a {shape} {dtype} tensor on cuda:{index} (got {tuple(out.shape)} {out.dtype} on "
                          f"{out.device})")
     if out.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError("out must have a unit inner stride")
@@ -194,15 +194,13 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, b_layo
     type.  Rows of no group keep what `out` holds (without `out`: undefined).
     Gradients, for dC of C's shape: of the rows gemm_grouped(dC, B, offsets, the other layout), of B
     gemm_grouped_wgrad(A, dC, offsets) for "kn" and gemm_grouped_wgrad(dC, A, offsets) for "nk"."""
-    _require(A, "A")
-    device = A.device
-    _require_stack(B, "B", device)
-    groups = _require_offsets(offsets, device)
+    index = A.get_device()
+    (M, K), st_a = _require_rows(A, "A", index)
+    shape_b, st_b = _require_rows(B, "B", index, 3)
+    groups = _require_offsets(offsets, index)
     ab = _AB_OF.get(A.dtype)
     if ab not in ("bf16", "f16") or B.dtype != A.dtype:
         raise ValueError("A and B must have the same dtype: bfloat16 or float16")
-    M, K = A.shape
-    shape_b = B.shape
     if b_layout == "nk":
         matrices, N, Kb = shape_b
     elif b_layout == "kn":
@@ -213,14 +211,14 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, b_layo
         raise ValueError(f"inner sizes differ: {K} vs {Kb}")
     if matrices != groups:
         raise ValueError(f"B holds {matrices} matrices, offsets {groups} groups")
-    with _Launch(device, stream) as handle:
-        out = _output(out, (M, N), out_dtype, ("f32", ab), device)
-        a, b, st_b = A.data_ptr(), B.data_ptr(), B.stride()
-        lda, ldb, sb = _pitch((M, K), A.stride()), _pitch(shape_b, st_b), st_b[0]
+    with _Launch(index, stream) as handle:
+        out = _output(out, (M, N), out_dtype, ("f32", ab), index)
+        a, b = A.data_ptr(), B.data_ptr()
+        lda, ldb, sb = _pitch((M, K), st_a), _pitch(shape_b, st_b), st_b[0]
         # whole 16-byte rows everywhere need no repack; the query knows the exact rule
         need = 0 if (lda | ldb | sb | K) % 8 == 0 and (a | b) % 16 == 0 else \
             tbg.gemm_grouped_workspace_query(groups, M, N, K, ab, a, lda, b, ldb, sb, b_layout)
-        ws_ptr, ws_bytes, held = _workspace(need, workspace, device)
+        ws_ptr, ws_bytes, held = _workspace(need, workspace, A.device)
         tbg.gemm_grouped(groups, M, N, K, offsets.data_ptr(), alpha, a, lda, b, ldb, sb, b_layout, ab, beta,
                          out.data_ptr(), _pitch((M, N), out.stride()), out_dtype, ws_ptr, ws_bytes, handle)
     return out
@@ -233,49 +231,48 @@ def gemm_grouped_wgrad(X: torch.Tensor, Y: torch.Tensor, offsets: torch.Tensor, 
     """C[e] = alpha·X[rows of e]ᵀ·Y[rows of e] + beta·C[e] through tbg_gemm_grouped_wgrad.  X: (M, P),
     Y: (M, Q), bf16 or fp16; out: (groups, P, Q) of type "f32" or X's.  An empty group's C is
     beta·C (zeros when beta == 0)."""
-    _require(X, "X")
-    device = X.device
-    _require(Y, "Y", device)
-    groups = _require_offsets(offsets, device)
+    index = X.get_device()
+    (M, P), st_x = _require_rows(X, "X", index)
+    (My, Q), st_y = _require_rows(Y, "Y", index)
+    groups = _require_offsets(offsets, index)
     ab = _AB_OF.get(X.dtype)
     if ab not in ("bf16", "f16") or Y.dtype != X.dtype:
         raise ValueError("X and Y must have the same dtype: bfloat16 or float16")
-    (M, P), (My, Q) = X.shape, Y.shape
     if My != M:
         raise ValueError(f"X has {M} rows, Y {My}")
-    with _Launch(device, stream) as handle:
-        out = _output(out, (groups, P, Q), out_dtype, ("f32", ab), device)
+    with _Launch(index, stream) as handle:
+        out = _output(out, (groups, P, Q), out_dtype, ("f32", ab), index)
         x, y, st_c = X.data_ptr(), Y.data_ptr(), out.stride()
-        ldx, ldy = _pitch((M, P), X.stride()), _pitch((M, Q), Y.stride())
+        ldx, ldy = _pitch((M, P), st_x), _pitch((M, Q), st_y)
         need = 0 if (ldx | ldy) % 8 == 0 and (x | y) % 16 == 0 else \
             tbg.gemm_grouped_wgrad_workspace_query(groups, M, P, Q, ab, x, ldx, y, ldy)
-        ws_ptr, ws_bytes, held = _workspace(need, workspace, device)
+        ws_ptr, ws_bytes, held = _workspace(need, workspace, X.device)
         tbg.gemm_grouped_wgrad(groups, M, P, Q, offsets.data_ptr(), alpha, x, ldx, y, ldy, ab, beta, out.data_ptr(),
                                _pitch((P, Q), st_c[1:]), st_c[0], out_dtype, ws_ptr, ws_bytes, handle)
     return out
 
 
-def _require_mx4(codes: torch.Tensor, scales: torch.Tensor, name: str, device: torch.device):
-    """Codes and scales that belong together; returns the codes' shape."""
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda:
-        raise ValueError(f"{name}'s codes and scales must be uint8 CUDA tensors")
-    if codes.device != device or scales.device != device:
-        raise ValueError(f"{name} is on {codes.device} and {scales.device}: every operand must be on one device")
-    shape, blocks = codes.shape, scales.shape
-    dims = len(shape)
-    if (dims not in (2, 3) or len(blocks) != dims or shape[0] != blocks[0] or shape[dims - 2] != blocks[dims - 2]
-            or shape[dims - 1] != 16 * blocks[dims - 1]):
-        raise ValueError(f"{name}: codes {tuple(shape)} and scales {tuple(blocks)} do not belong together (matrices or "
-                         "stacks, 16 bytes of codes and one scale per 32 values)")
-    if (codes.stride(-1) != 1 and shape[-1] > 1) or (scales.stride(-1) != 1 and blocks[-1] > 1):
+def _require_mx4(codes: torch.Tensor, scales: torch.Tensor, name: str, index: int, dims=(2, 3)):
+    """Codes and scales that belong together, on device `index`: the codes' shape and both pitches in
+    bytes (a single row's pitch is its length rounded up to 16)."""
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"{name}'s codes and scales must be uint8 tensors")
+    if index < 0 or codes.get_device() != index or scales.get_device() != index:
+        raise ValueError(f"{name} is on {codes.device} and {scales.device}: every operand must be on one CUDA (HIP) "
+                         "device")
+    shape, blocks, st, st_s = codes.shape, scales.shape, codes.stride(), scales.stride()
+    n = len(shape)
+    if n not in dims or len(blocks) != n:
+        raise ValueError(f"{name}'s codes and scales must have {' or '.join(map(str, dims))} dimensions")
+    rows, half, nb = shape[n - 2], shape[n - 1], blocks[n - 1]
+    if shape[0] != blocks[0] or rows != blocks[n - 2] or half != 16 * nb:
+        raise ValueError(f"{name}: codes {tuple(shape)} and scales {tuple(blocks)} do not belong together (16 bytes of "
+                         "codes and one scale per 32 values)")
+    if (st[n - 1] != 1 and half > 1) or (st_s[n - 1] != 1 and nb > 1):
         raise ValueError(f"{name}'s codes and scales must have a unit inner stride")
-    return shape
-
-
-def _mx4_pitch(t: torch.Tensor) -> int:
-    """Row pitch in bytes, of a single row its length rounded up to 16."""
-    shape = t.shape
-    return t.stride(-2) if shape[-2] > 1 else -(-shape[-1] // 16) * 16
+    if rows > 1:
+        return shape, st[n - 2], st_s[n - 2]
+    return shape, half, -(-nb // 16) * 16
 
 
 def _flat_rows(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -290,32 +287,44 @@ def _flat_rows(t: torch.Tensor, name: str) -> torch.Tensor:
     return t.as_strided((n * rows, cols), (t.stride(1), t.stride(2)))
 
 
+def _mx4_rows(codes: torch.Tensor, scales: torch.Tensor, index: int):
+    """Rows, codes and scales of a matrix or a stack as one matrix: (rows, codes address, pitch, scales
+    address, pitch)."""
+    codes, scales = _flat_rows(codes, "codes"), _flat_rows(scales, "scales")
+    shape, ld_c, ld_s = _require_mx4(codes, scales, "codes", index, (2,))
+    return shape[0], codes.data_ptr(), ld_c, scales.data_ptr(), ld_s
+
+
 def mx4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                  stream: Optional[torch.cuda.Stream] = None):
     """Rows of x, (rows, cols) or a stack (n, rows, cols) of fp32, bf16 or fp16, as microscaled 4-bit
     data through tbg_mx4_quantize.  Returns (codes, scales), uint8: two codes per byte, one scale per
     32 values, cols rounded up to whole blocks (zeros).  The scales' rows are 16-byte pitched."""
-    x_dtype = _X_OF.get(x.dtype)
-    if not x.is_cuda or x.dim() not in (2, 3) or x_dtype is None:
+    index, x_dtype = x.get_device(), _X_OF.get(x.dtype)
+    if index < 0 or x.dim() not in (2, 3) or x_dtype is None:
         raise ValueError("x must be a 2-D or 3-D float32, bfloat16 or float16 CUDA tensor")
-    if x.stride(-1) != 1 and x.shape[-1] > 1:
+    x2 = _flat_rows(x, "x")
+    (rows, cols), st = x2.shape, x2.stride()
+    if st[1] != 1 and cols > 1:
         raise ValueError("x must have a unit inner stride")
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales must be given together")
-    device, lead, cols = x.device, x.shape[:-1], x.shape[-1]
     blocks = -(-cols // 32)
-    with _Launch(device, stream) as handle:
+    with _Launch(index, stream) as handle:
         if codes is None:
-            pitch = -(-blocks // 16) * 16
-            codes = torch.empty((*lead, 16 * blocks), dtype=torch.uint8, device=device)
-            scales = torch.empty((*lead, pitch), dtype=torch.uint8, device=device)
-            if pitch != blocks:
-                scales = scales[..., :blocks]
-        elif _require_mx4(codes, scales, "x", device) != (*lead, 16 * blocks):
-            raise ValueError(f"codes must be {(*lead, 16 * blocks)} (got {tuple(codes.shape)})")
-        x2, c2, s2 = _flat_rows(x, "x"), _flat_rows(codes, "codes"), _flat_rows(scales, "scales")
-        tbg.mx4_quantize(x2.shape[0], cols, x2.data_ptr(), _pitch(x2.shape, x2.stride()), x_dtype, c2.data_ptr(),
-                         _mx4_pitch(c2), s2.data_ptr(), _mx4_pitch(s2), handle)
+            ld_c, ld_s = 16 * blocks, -(-blocks // 16) * 16
+            codes = torch.empty((rows, ld_c), dtype=torch.uint8, device=index)
+            scales = torch.empty_strided((rows, blocks), (ld_s, 1), dtype=torch.uint8, device=index)
+            c, s = codes.data_ptr(), scales.data_ptr()
+            if x2 is not x:
+                n, per = x.shape[0], x.shape[1]
+                codes = codes.view(n, per, ld_c)
+                scales = scales.as_strided((n, per, blocks), (per * ld_s, ld_s, 1))
+        else:
+            if tuple(codes.shape) != (*x.shape[:-1], 16 * blocks):
+                raise ValueError(f"codes must be {(*x.shape[:-1], 16 * blocks)} (got {tuple(codes.shape)})")
+            _, c, ld_c, s, ld_s = _mx4_rows(codes, scales, index)
+        tbg.mx4_quantize(rows, cols, x2.data_ptr(), _pitch((rows, cols), st), x_dtype, c, ld_c, s, ld_s, handle)
     return codes, scales
 
 
@@ -323,16 +332,20 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: Optional[int
                    out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The values of mx4_quantize's codes and scales through tbg_mx4_dequantize: the first `cols`
     columns (default: all), of type "f32", "bf16" or "f16"."""
-    device = codes.device
-    *lead, half = _require_mx4(codes, scales, "codes", device)
+    index = codes.get_device()
+    shape, ld_c, ld_s = _require_mx4(codes, scales, "codes", index)
+    *lead, half = shape
     cols = 2 * half if cols is None else int(cols)
     if not (2 * half - 32 < cols <= 2 * half):
         raise ValueError(f"cols must end in the last block of 32: {max(0, 2 * half - 31)}..{2 * half} (got {cols})")
-    with _Launch(device, stream) as handle:
-        out = _output(out, (*lead, cols), out_dtype, ("f32", "bf16", "f16"), device)
-        o2, c2, s2 = _flat_rows(out, "out"), _flat_rows(codes, "codes"), _flat_rows(scales, "scales")
-        tbg.mx4_dequantize(o2.shape[0], cols, c2.data_ptr(), _mx4_pitch(c2), s2.data_ptr(), _mx4_pitch(s2),
-                           o2.data_ptr(), _pitch(o2.shape, o2.stride()), out_dtype, handle)
+    with _Launch(index, stream) as handle:
+        out = _output(out, (*lead, cols), out_dtype, ("f32", "bf16", "f16"), index)
+        o2, rows, c, s = out, shape[0], codes.data_ptr(), scales.data_ptr()
+        if len(shape) == 3:
+            o2 = _flat_rows(out, "out")
+            rows, c, ld_c, s, ld_s = _mx4_rows(codes, scales, index)
+        tbg.mx4_dequantize(rows, cols, c, ld_c, s, ld_s, o2.data_ptr(), _pitch(o2.shape, o2.stride()), out_dtype,
+                           handle)
     return out
 
 
@@ -342,18 +355,15 @@ def mx4_gemm(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scales:
     """C = alpha·A·Bᵀ + beta·C for microscaled 4-bit A (M, K/2 codes) and B (N, K/2 codes), each with
     its scales (rows, K/32), through tbg_mx4_gemm.  Codes and scales 16-byte aligned and pitched, as
     mx4_quantize makes them."""
-    device = A.device
-    shape_a, shape_b = _require_mx4(A, a_scales, "A", device), _require_mx4(B, b_scales, "B", device)
-    if len(shape_a) != 2 or len(shape_b) != 2:
-        raise ValueError("A and B must be matrices (mx4_gemm_grouped takes stacks)")
-    (M, half), (N, half_b) = shape_a, shape_b
+    index = A.get_device()
+    (M, half), lda, ld_as = _require_mx4(A, a_scales, "A", index, (2,))
+    (N, half_b), ldb, ld_bs = _require_mx4(B, b_scales, "B", index, (2,))
     if half != half_b:
         raise ValueError(f"inner sizes differ: {2 * half} vs {2 * half_b}")
-    with _Launch(device, stream) as handle:
-        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), device)
-        tbg.mx4_gemm(M, N, 2 * half, alpha, A.data_ptr(), _mx4_pitch(A), a_scales.data_ptr(), _mx4_pitch(a_scales),
-                     B.data_ptr(), _mx4_pitch(B), b_scales.data_ptr(), _mx4_pitch(b_scales), beta, out.data_ptr(),
-                     _pitch((M, N), out.stride()), out_dtype, handle)
+    with _Launch(index, stream) as handle:
+        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), index)
+        tbg.mx4_gemm(M, N, 2 * half, alpha, A.data_ptr(), lda, a_scales.data_ptr(), ld_as, B.data_ptr(), ldb,
+                     b_scales.data_ptr(), ld_bs, beta, out.data_ptr(), _pitch((M, N), out.stride()), out_dtype, handle)
     return out
 
 
@@ -363,22 +373,19 @@ def mx4_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b
     """mx4_gemm for the rows of every group (offsets as gemm_grouped) with its own B, (groups, N, K/2
     codes), through tbg_mx4_gemm_grouped.  Rows of no group keep what `out` holds (without `out`:
     undefined)."""
-    device = A.device
-    shape_a, shape_b = _require_mx4(A, a_scales, "A", device), _require_mx4(B, b_scales, "B", device)
-    groups = _require_offsets(offsets, device)
-    if len(shape_a) != 2 or len(shape_b) != 3:
-        raise ValueError("A must be a matrix and B a stack of matrices")
-    (M, half), (matrices, N, half_b) = shape_a, shape_b
+    index = A.get_device()
+    (M, half), lda, ld_as = _require_mx4(A, a_scales, "A", index, (2,))
+    (matrices, N, half_b), ldb, ld_bs = _require_mx4(B, b_scales, "B", index, (3,))
+    groups = _require_offsets(offsets, index)
     if half != half_b:
         raise ValueError(f"inner sizes differ: {2 * half} vs {2 * half_b}")
     if matrices != groups:
         raise ValueError(f"B holds {matrices} matrices, offsets {groups} groups")
-    with _Launch(device, stream) as handle:
-        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), device)
-        tbg.mx4_gemm_grouped(groups, M, N, 2 * half, offsets.data_ptr(), alpha, A.data_ptr(), _mx4_pitch(A),
-                             a_scales.data_ptr(), _mx4_pitch(a_scales), B.data_ptr(), _mx4_pitch(B), B.stride(0),
-                             b_scales.data_ptr(), _mx4_pitch(b_scales), b_scales.stride(0), beta, out.data_ptr(),
-                             _pitch((M, N), out.stride()), out_dtype, handle)
+    with _Launch(index, stream) as handle:
+        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), index)
+        tbg.mx4_gemm_grouped(groups, M, N, 2 * half, offsets.data_ptr(), alpha, A.data_ptr(), lda, a_scales.data_ptr(),
+                             ld_as, B.data_ptr(), ldb, B.stride(0), b_scales.data_ptr(), ld_bs, b_scales.stride(0),
+                             beta, out.data_ptr(), _pitch((M, N), out.stride()), out_dtype, handle)
     return out
 
 
