@@ -489,6 +489,53 @@ def test_offsets_out_of_order_or_range_stay_inside_the_operands():
 
 
 @gpu
+@pytest.mark.parametrize("groups,rows,empty_every", [(1000, 3000, 3), (4096, 5000, 2), (65, 64, 0)])
+def test_many_groups(groups, rows, empty_every):
+    gen, dt = _gen(groups), torch.bfloat16
+    rng = np.random.default_rng(groups)
+    sizes = rng.multinomial(rows, np.ones(groups) / groups)
+    if empty_every:
+        sizes[::empty_every] = 0
+    edges = _offsets(sizes, 2)
+    A, B = _ints(gen, (edges[-1] + 3, 24), dt), _ints(gen, (groups, 16, 24), dt)
+    want = _ref_rows(A, B, edges, "nk")
+    out = _ops().gemm_grouped(A, B, _dev(edges), "nk", "f32", out=torch.zeros((edges[-1] + 3, 16), device="cuda"))
+    assert torch.equal(out.double(), want)
+    g = _ops().gemm_grouped_wgrad(A, A, _dev(edges))
+    assert torch.equal(g.double(), _ref_wgrad(A, A, edges))
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """Rows at the largest pitch and matrices 4 GiB apart: operands whose byte offsets pass 2^32, laid
+    over one buffer with NaN where nothing may be read (small enough pieces are written)."""
+    dt, gen = torch.bfloat16, _gen(61)
+    pitch, M, N, K = (1 << 22) - 8, 600, 24, 40  # 600 rows of 8 MiB: 5 GB
+    buf = torch.empty(pitch * M, dtype=dt, device="cuda")
+    A = buf.as_strided((M, K), (pitch, 1))
+    A.copy_(_ints(gen, (M, K), dt))
+    B = _ints(gen, (2, N, K), dt)
+    edges = [0, 590, 600]
+    out = _ops().gemm_grouped(A, B, _dev(edges), "nk", "f32")
+    assert torch.equal(out.double(), _ref_rows(A, B, edges, "nk"))
+    g = _ops().gemm_grouped_wgrad(A, _ints(gen, (M, N), dt), _dev(edges))
+    assert g.isfinite().all()
+    Y = _ints(gen, (M, N), dt)
+    assert torch.equal(_ops().gemm_grouped_wgrad(Y, A, _dev(edges)).double(), _ref_wgrad(Y, A, edges))
+    for layout, shape in (("nk", (N, K)), ("kn", (K, N))):
+        stride = (1 << 31) + 64  # elements: the second matrix lies 4 GiB and a little behind
+        W = buf.as_strided((2, *shape), (stride, shape[1], 1))
+        W.copy_(_ints(gen, (2, *shape), dt))
+        X = _ints(gen, (30, K), dt)
+        out = _ops().gemm_grouped(X, W, _dev([0, 11, 30]), layout, "f32")
+        assert torch.equal(out.double(), _ref_rows(X, W, [0, 11, 30], layout))
+    C = buf.view(torch.float32).as_strided((2, N, K), ((1 << 30) + 128, K, 1))
+    X, Y = _ints(gen, (30, N), dt), _ints(gen, (30, K), dt)
+    _ops().gemm_grouped_wgrad(X, Y, _dev([0, 11, 30]), "f32", out=C)
+    assert torch.equal(C.double(), _ref_wgrad(X, Y, [0, 11, 30]))
+
+
+@gpu
 def test_torch_helper_refusals():
     ops, dt = _ops(), torch.bfloat16
     A, B = torch.zeros((8, 16), dtype=dt, device="cuda"), torch.zeros((2, 16, 24), dtype=dt, device="cuda")

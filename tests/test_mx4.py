@@ -377,6 +377,30 @@ def test_grouped_product_exact(case):
 
 
 @gpu
+@pytest.mark.parametrize("M", [9, 600])
+def test_product_offsets_past_32_bits(M):
+    """Codes at nearly the largest pitch (600 rows of 8 MiB) and matrices 4 GiB apart, scales too."""
+    rng, K, N = np.random.default_rng(M), 288, 40
+    a, sa, va = _random_mx4(rng, (M,), K)
+    b, sb, vb = _random_mx4(rng, (2, N), K)
+    buf = torch.empty(5 << 30, dtype=torch.uint8, device="cuda")
+    pitch = (1 << 23) - 16
+    A = buf.as_strided((M, K // 2), (pitch, 1))
+    A.copy_(a)
+    out = _ops().mx4_gemm(A, sa, b[0], sb[0], "f32")
+    assert torch.equal(out.double(), va @ vb[0].t().contiguous())
+    big = buf.as_strided((2, N, K // 2), ((1 << 32) + 64, K // 2, 1))
+    big.copy_(b)
+    big_s = buf[1 << 20:].as_strided((2, N, K // 32), ((1 << 32) + 4096, 16, 1))
+    big_s.copy_(sb)
+    cut = M // 2
+    off = torch.tensor([0, cut, M], dtype=torch.int32, device="cuda")
+    out = _ops().mx4_gemm_grouped(a, sa, big, big_s, off, "f32")
+    want = torch.cat([va[:cut] @ vb[0].t().contiguous(), va[cut:] @ vb[1].t().contiguous()])
+    assert torch.equal(out.double(), want)
+
+
+@gpu
 def test_quantised_experts_as_a_server_runs_them():
     """Weights quantised once; each step quantises its rows and multiplies, captured and replayed with
     other rows and other offsets.  Every replay equals the eager result bit for bit, and the eager
