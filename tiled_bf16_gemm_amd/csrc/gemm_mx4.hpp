@@ -12,11 +12,13 @@
 //    241 against 234 µs, 2048³ 11.4 against 11.0).  Both 16-byte halves of rows 8..15 of 16 are exchanged in LDS, so that a
 //    fragment's 16 rows, 32 bytes apart, are read from distinct banks.  The instruction takes a lane's
 //    scale from one byte of a register, chosen by an immediate.
-//  * Placement.  Lane l multiplies row l%16 and, in k-step kk, block 2(l/16)+kk of the tile (not
-//    4kk + l/16): its two k-steps then need two neighbouring scale bytes, one 16-bit LDS read per
-//    fragment and K tile.  The sum runs over the tile's blocks in another order, the same for A
-//    and B.  The copies place block 2g+kk of a row where the 16-bit kernels have chunk 4kk+g, so
-//    the fragment reads, free of bank conflicts, are unchanged.
+//  * Placement.  Lane l multiplies row l%16 and, in k-step kk, block 2·pair(l/16)+kk of the tile
+//    (not 4kk + l/16): its two k-steps then need two neighbouring scale bytes, one 16-bit LDS read
+//    per fragment and K tile.  The sum runs over the tile's blocks in another order, the same for A
+//    and B.  pair = 0, 3, 1, 2: the 16-byte read serves lanes 0-3, 12-15, 20-27 (and the like)
+//    together, whose rows' 2-row swizzle keeps two columns apart in the banks only if their numbers
+//    differ by an exclusive or of 1, 6 or 7; 2·pair of neighbouring lane groups differ by 6.  The
+//    copies stay in the rows' own order.
 // Bounds: rows past the tile and code chunks past K are masked copies (zero codes); scale rows past
 // the tile too, and scale bytes past the last block, whatever the row's padding holds, are zeroed
 // in registers in the tiles at the end of K (a NaN scale would turn zero codes into NaN).
@@ -94,21 +96,19 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
   constexpr int FM = T::FM, AT = T::AtomsA, BT = T::AtomsB, A = T::Atoms, P = T::Products, R = T::Reads;
   constexpr int SA = C::ScaleAtoms;
   const int ktiles = box.blocks > 0 ? (box.blocks + 7) / 8 : 1;
-  const int g = lane >> 4;
+  const int pair = (0x2130 >> (4 * (lane >> 4))) & 15;  // 0, 3, 1, 2 (lane groups 0..3)
 
-  // Codes: atom slot p of a row holds block 2(p%4) + p/4.
   LaneChunk la[AT], lb[BT];
-  auto code_lanes = [&](LaneChunk& lc, int row, uint32_t pitch, int lines) __attribute__((always_inline)) {
-    const LaneChunk s = lane_chunk<kSwizzle128B2Row>(row, lane, 0);
-    const int block = 2 * (s.chunk & 3) + (s.chunk >> 2);
-    lc.chunk = block;
-    lc.offset = (uint32_t)(row + (lane >> 3)) * pitch + (uint32_t)block * 16u;
-    mask_row(lc, row + (lane >> 3), lines);
-  };
 #pragma unroll
-  for (int i = 0; i < AT; ++i) code_lanes(la[i], 8 * (AT * wave + i), box.pitch_a, box.rows_a);
+  for (int i = 0; i < AT; ++i) {
+    la[i] = lane_chunk<kSwizzle128B2Row>(8 * (AT * wave + i), lane, box.pitch_a);
+    mask_row(la[i], 8 * (AT * wave + i) + (lane >> 3), box.rows_a);
+  }
 #pragma unroll
-  for (int i = 0; i < BT; ++i) code_lanes(lb[i], 8 * (BT * wave + i), box.pitch_b, box.rows_b);
+  for (int i = 0; i < BT; ++i) {
+    lb[i] = lane_chunk<kSwizzle128B2Row>(8 * (BT * wave + i), lane, box.pitch_b);
+    mask_row(lb[i], 8 * (BT * wave + i) + (lane >> 3), box.rows_b);
+  }
   // Scales: two lanes per row, the halves exchanged in rows 8..15 of 16.
   uint32_t ls[SA];
   const int line0 = C::RowsWave * wave;  // this wave's first scale row: all A's or all B's
@@ -160,14 +160,16 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
   };
 
   const int wm = wave >> 1, wn = wave & 1;
-  const FragAddr<T> fa = make_frag_addr<T>(wm, wn, lane);
+  // Fragment rows start at multiples of 16, so the swizzle is the lane's own.
+  const uint32_t lane_row = (uint32_t)(lane & 15) * 128u, swz = (lane >> 1) & 7;
+  const uint32_t col[2] = {lane_row + ((2 * pair) ^ swz) * 16u, lane_row + ((2 * pair + 1) ^ swz) * 16u};
   auto read = [&](Mx4Frags& f, const uint8_t* s, int kk, int i) __attribute__((always_inline)) {
-    if (i < FM) f.a[i] = *(const i32x4_t*)(s + fa.a_lane + i * 2048 + fa.a_col[kk]);
-    else f.b[i - FM] = *(const i32x4_t*)(s + T::ABytes + fa.b_lane + (i - FM) * 2048 + fa.b_col[kk]);
+    if (i < FM) f.a[i] = *(const i32x4_t*)(s + wm * T::TM * 128 + i * 2048 + col[kk]);
+    else f.b[i - FM] = *(const i32x4_t*)(s + T::ABytes + wn * T::TN * 128 + (i - FM) * 2048 + col[kk]);
   };
-  // Scale bytes of fragment i for K tile `quad`, QT (0..3): blocks 2g and 2g+1 of the row.
+  // Scale bytes of fragment i for K tile `quad`, QT (0..3): blocks 2·pair and 2·pair+1.
   const uint8_t* const scales = smem + S * T::StageBytes;
-  const int lane_s = (lane & 15) * 32 + 2 * g, swap = (lane >> 3) & 1;
+  const int lane_s = (lane & 15) * 32 + 2 * pair, swap = (lane >> 3) & 1;
   auto read_scale = [&](uint32_t (&s)[R], int quad, auto qt, int i) __attribute__((always_inline)) {
     constexpr int QT = decltype(qt)::value;
     const uint8_t* buf = scales + (quad & 1) * C::QuadBytes + lane_s + ((QT >> 1) ^ swap) * 16 + (QT & 1) * 8;
@@ -177,7 +179,7 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
   // reads: products written as assembly must not follow a vector instruction that writes their
   // operand directly.
   auto mask_scales = [&](uint32_t (&s)[R], int kt) __attribute__((always_inline)) {
-    const int left = box.blocks - kt * 8 - 2 * g;
+    const int left = box.blocks - kt * 8 - 2 * pair;
     const uint32_t keep = left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
