@@ -479,7 +479,7 @@ tbg_status mx4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, const 
                   (ll)(ragged ? groups : 1), (ll)M, (ll)N, (ll)K, c_dtype == TBG_F32 ? "f32" : "bf16",
                   few ? "rows" : "ring", few ? 16 : bm, few ? 16 : bn, few ? 1 : stages);
   const hipError_t e = few ? tbg::launch_few_rows(p, 2, out_code(c_dtype), (hipStream_t)stream)
-                           : tbg::launch_mx4_gemm(p, bm, bn, stages, c_dtype == TBG_BF16, (hipStream_t)stream);
+                           : tbg::launch_mx4_gemm(p, bm, bn, stages, c_dtype == TBG_BF16, cus, (hipStream_t)stream);
   if (e != hipSuccess) return fail(TBG_ERR_HIP, "mx4 gemm launch: %s", hipGetErrorString(e));
   return TBG_OK;
 }

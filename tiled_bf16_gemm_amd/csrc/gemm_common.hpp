@@ -237,19 +237,25 @@ __device__ __forceinline__ void kstep(f32x4_t (&acc)[T::FN][T::FM], const Frags<
   }
 }
 
-// The wait states between the K loop's last product and the first read of an accumulator, for
-// products issued as inline assembly (the compiler cannot see their hazards; for its builtin it
-// inserts the waits itself).  The drain is one assembly statement; each accumulator then passes
-// through an empty statement that claims to rewrite it, so every later read of it depends on a
-// statement that the compiler keeps after the drain.
+// Every accumulator passes through an empty statement that claims to rewrite it: later reads of it
+// depend on a statement that the compiler keeps in its place.
 template <class T>
-__device__ __forceinline__ void drain_acc(f32x4_t (&acc)[T::FN][T::FM]) {
-  if (!T::AsmMfma) return;
-  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+a"(acc[0][0]));
+__device__ __forceinline__ void keep_acc(f32x4_t (&acc)[T::FN][T::FM]) {
 #pragma unroll
   for (int i = 0; i < T::FN; ++i)
 #pragma unroll
     for (int j = 0; j < T::FM; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+// The wait states between the K loop's last product and the first read of an accumulator, for
+// products issued as inline assembly (the compiler cannot see their hazards; for its builtin it
+// inserts the waits itself).  The drain is one assembly statement, and keep_acc holds every later
+// read behind it.
+template <class T>
+__device__ __forceinline__ void drain_acc(f32x4_t (&acc)[T::FN][T::FM]) {
+  if (!T::AsmMfma) return;
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+a"(acc[0][0]));
+  keep_acc<T>(acc);
 }
 
 // LDS chunk swizzle of the epilogue's park: rows of `cpr` 16-byte chunks; XOR the chunk index
@@ -291,29 +297,33 @@ __device__ __forceinline__ typename Half4<OUT>::vec round4(const f32x4_t& v) {
 // so it should not push operand tiles out of the caches.  OUT: 0 fp32, 1 bf16, 2 fp16.  With SCALED the park keeps the fp32
 // sums and each piece becomes alpha·S + beta·C_old (C_old read only when beta != 0) before it is
 // rounded to C's type ("GEMM" page, tensor-core section: C <- alpha·A·B + beta·C).
-template <class T, int OUT, int SCALED>
+// PARK: bytes of LDS the wave parks in (a quarter of the ring; less splits the block into more bands of
+// rows, and into column parts where 16 whole rows do not fit).
+template <class T, int OUT, int SCALED, int PARK = T::RingBytes / 4>
 __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[T::FN][T::FM], uint8_t* park, const GemmParams& p,
                                           int row0, int col0, int lane) {
   constexpr int ES = OUT != 0 ? 2 : 4;                     // element size of C
   constexpr int PES = (OUT != 0 && !SCALED) ? 2 : 4;       // element size in the park
-  constexpr int RowBytes = T::TN * PES;
+  constexpr int Cols = T::TN * PES * 16 <= PARK ? T::TN : PARK / 16 / PES;  // columns per part
+  constexpr int Parts = T::TN / Cols, PartFN = T::FN / Parts;
+  constexpr int RowBytes = Cols * PES;
   constexpr int CPR = RowBytes / 16;
   constexpr int EPC = 16 / PES;  // elements per 16-byte park chunk
-  constexpr int ParkBytes = T::RingBytes / 4;
-  constexpr int Bands = (T::TM * RowBytes + ParkBytes - 1) / ParkBytes;
+  constexpr int Bands = (T::TM * RowBytes + PARK - 1) / PARK;
   constexpr int BandFM = T::FM / Bands;
   constexpr int BandRows = 16 * BandFM;
   constexpr int RowsPerRead = 64 / CPR;
   constexpr int ReadsPerBand = BandRows / RowsPerRead;
-  static_assert(T::FM % Bands == 0 && BandRows % RowsPerRead == 0, "epilogue bands");
+  static_assert(T::FM % Bands == 0 && BandRows % RowsPerRead == 0 && T::FN % Parts == 0, "epilogue bands");
 #pragma unroll
-  for (int band = 0; band < Bands; ++band) {
+  for (int bp = 0; bp < Bands * Parts; ++bp) {
+    const int band = bp / Parts, part = bp % Parts;
 #pragma unroll
     for (int f = 0; f < BandFM; ++f)
 #pragma unroll
-      for (int fn = 0; fn < T::FN; ++fn) {
+      for (int fn = 0; fn < PartFN; ++fn) {
         const int r = 16 * f + (lane & 15);
-        const f32x4_t v = acc[fn][band * BandFM + f];
+        const f32x4_t v = acc[part * PartFN + fn][band * BandFM + f];
         if constexpr (PES == 2) {
           const int c = 2 * fn + (lane >> 5);
           const auto h = round4<OUT>(v);
@@ -328,7 +338,7 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[T::FN][T::FM], u
     for (int i = 0; i < ReadsPerBand; ++i) {
       const int r = RowsPerRead * i + lane / CPR, c = lane % CPR;
       const uint4 v = *(const uint4*)(park + r * RowBytes + ((c ^ park_xor<CPR>(r)) << 4));
-      const int gm = row0 + BandRows * band + r, gn = col0 + EPC * c;
+      const int gm = row0 + BandRows * band + r, gn = col0 + Cols * part + EPC * c;
       if (gm >= p.M) continue;
       uint8_t* dst = (uint8_t*)p.C + ((uint64_t)gm * p.ldc + gn) * ES;
       const bool whole = p.vec_store && gn + EPC - 1 < p.N;
@@ -400,7 +410,7 @@ __device__ __forceinline__ void store_tile(const f32x4_t (&acc)[T::FN][T::FM], u
       }
     }
     // The next band's writes follow these reads in this wave's LDS order.
-    if (Bands > 1) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (Bands * Parts > 1) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 

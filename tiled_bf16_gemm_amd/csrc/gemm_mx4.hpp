@@ -84,81 +84,115 @@ struct Mx4Frags {
   i32x4_t a[8], b[8];
 };
 
-// acc += A·Bᵀ over one workgroup tile.  Schedule of the barrier ring, four K tiles (a quad) per
-// iteration; the first two tiles of a quad bring the next quad's scales along, half each, and
-// k-step 1 reads the next tile's scales next to its first fragments.  A barrier lets the code atoms
-// of the S-2 tiles behind the awaited one be in flight; scale atoms among them (a wave's own number)
-// only make it wait for a few more copies than it needs.
+// The copies of one workgroup tile: the wave's lanes of every atom, and the atoms of a K tile.
 template <class C, int S>
-__device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uint8_t* smem, const Mx4Box& box,
-                                         int wave, int lane) {
+struct Mx4Copies {
   using T = typename C::T;
-  constexpr int FM = T::FM, AT = T::AtomsA, BT = T::AtomsB, A = T::Atoms, P = T::Products, R = T::Reads;
-  constexpr int SA = C::ScaleAtoms;
-  const int ktiles = box.blocks > 0 ? (box.blocks + 7) / 8 : 1;
-  const int pair = (0x2130 >> (4 * (lane >> 4))) & 15;  // 0, 3, 1, 2 (lane groups 0..3)
-
-  LaneChunk la[AT], lb[BT];
-#pragma unroll
-  for (int i = 0; i < AT; ++i) {
-    la[i] = lane_chunk<kSwizzle128B2Row>(8 * (AT * wave + i), lane, box.pitch_a);
-    mask_row(la[i], 8 * (AT * wave + i) + (lane >> 3), box.rows_a);
-  }
-#pragma unroll
-  for (int i = 0; i < BT; ++i) {
-    lb[i] = lane_chunk<kSwizzle128B2Row>(8 * (BT * wave + i), lane, box.pitch_b);
-    mask_row(lb[i], 8 * (BT * wave + i) + (lane >> 3), box.rows_b);
-  }
-  // Scales: two lanes per row, the halves exchanged in rows 8..15 of 16.
-  uint32_t ls[SA];
-  const int line0 = C::RowsWave * wave;  // this wave's first scale row: all A's or all B's
-  const bool scales_a = line0 < T::BM, has_scales = line0 < C::Rows;
-  const uint32_t pitch_s = scales_a ? box.pitch_as : box.pitch_bs;
-#pragma unroll
-  for (int i = 0; i < SA; ++i) {
-    const int row = line0 - (scales_a ? 0 : T::BM) + 32 * i + (lane >> 1);
-    const uint32_t half = (uint32_t)((lane & 1) ^ ((lane >> 4) & 1));
-    ls[i] = row >= (scales_a ? box.rows_a : box.rows_b) ? kOobOffset : (uint32_t)row * pitch_s + half * 16u;
-  }
-  const rsrc_t rs0 = scales_a ? box.ras : box.rbs;
-
-  const uint32_t smem_addr = lds_addr_of(smem);
-  const uint32_t scale_addr = smem_addr + S * T::StageBytes + line0 * 32;
+  static constexpr int AT = T::AtomsA, BT = T::AtomsB, A = T::Atoms, SA = C::ScaleAtoms;
   struct Copy {
     rsrc_t ra, rb, rs;
     uint32_t lds_a, lds_b, lds_s;
     int valid;
     bool live_s;
   };
-  auto make_copy = [&](int kt, int stage) __attribute__((always_inline)) {
+  Mx4Box box;
+  LaneChunk la[AT], lb[BT];
+  uint32_t ls[SA];
+  rsrc_t rs0;
+  uint32_t ring, scales;  // LDS addresses: the ring; this wave's first scale row
+  int wave;
+
+  __device__ __forceinline__ void set(const Mx4Box& b, const uint8_t* smem, int wave_, int lane) {
+    box = b;
+    wave = wave_;
+#pragma unroll
+    for (int i = 0; i < AT; ++i) {
+      la[i] = lane_chunk<kSwizzle128B2Row>(8 * (AT * wave + i), lane, box.pitch_a);
+      mask_row(la[i], 8 * (AT * wave + i) + (lane >> 3), box.rows_a);
+    }
+#pragma unroll
+    for (int i = 0; i < BT; ++i) {
+      lb[i] = lane_chunk<kSwizzle128B2Row>(8 * (BT * wave + i), lane, box.pitch_b);
+      mask_row(lb[i], 8 * (BT * wave + i) + (lane >> 3), box.rows_b);
+    }
+    // Scales: two lanes per row, the halves exchanged in rows 8..15 of 16.
+    const int line0 = C::RowsWave * wave;  // this wave's first scale row: all A's or all B's
+    const bool of_a = line0 < T::BM;
+    const uint32_t pitch_s = of_a ? box.pitch_as : box.pitch_bs;
+#pragma unroll
+    for (int i = 0; i < SA; ++i) {
+      const int row = line0 - (of_a ? 0 : T::BM) + 32 * i + (lane >> 1);
+      const uint32_t half = (uint32_t)((lane & 1) ^ ((lane >> 4) & 1));
+      ls[i] = row >= (of_a ? box.rows_a : box.rows_b) ? kOobOffset : (uint32_t)row * pitch_s + half * 16u;
+    }
+    rs0 = of_a ? box.ras : box.rbs;
+    ring = lds_addr_of(smem);
+    scales = ring + S * T::StageBytes + line0 * 32;
+  }
+
+  __device__ __forceinline__ Copy tile(int kt, int stage) const {
     Copy c;
     const uint64_t off = (uint64_t)kt * 128u;
     c.ra = rsrc_advance(box.ra, off);
     c.rb = rsrc_advance(box.rb, off);
     c.valid = box.blocks - kt * 8;
-    c.lds_a = smem_addr + stage * T::StageBytes + AT * wave * 1024;
-    c.lds_b = smem_addr + stage * T::StageBytes + T::ABytes + BT * wave * 1024;
+    c.lds_a = ring + stage * T::StageBytes + AT * wave * 1024;
+    c.lds_b = ring + stage * T::StageBytes + T::ABytes + BT * wave * 1024;
     return c;
-  };
-  auto scale_copy = [&](Copy& c, int quad) __attribute__((always_inline)) {
-    c.rs = rsrc_advance(rs0, (uint64_t)quad * 32u);
-    c.rs.z = max(rs0.z - quad * 32, 0);
-    c.live_s = quad * 32 < box.blocks;
-    c.lds_s = scale_addr + (quad & 1) * C::QuadBytes;
-  };
+  }
+  __device__ __forceinline__ void quad(Copy& c, int q) const {
+    c.rs = rsrc_advance(rs0, (uint64_t)q * 32u);
+    c.rs.z = max(rs0.z - q * 32, 0);
+    c.live_s = q * 32 < box.blocks;
+    c.lds_s = scales + (q & 1) * C::QuadBytes;
+  }
   // atoms 0..A-1: codes; A + i: scale atom i
-  auto atom = [&](const Copy& c, int j, auto interior) __attribute__((always_inline)) {
-    constexpr bool in = decltype(interior)::value;
+  template <bool INTERIOR>
+  __device__ __forceinline__ void atom(const Copy& c, int j) const {
     if (j < AT) {
-      issue_atom_if(c.ra, c.lds_a, j * 1024, la[j].offset, in || la[j & 1].chunk < c.valid);
+      issue_atom_if(c.ra, c.lds_a, j * 1024, la[j].offset, INTERIOR || la[j & 1].chunk < c.valid);
     } else if (j < A) {
       const int i = j - AT;
-      issue_atom_if(c.rb, c.lds_b, i * 1024, lb[i].offset, in || lb[i & 1].chunk < c.valid);
-    } else if (C::RowsWave * 4 == C::Rows || has_scales) {
-      issue_atom_if(c.rs, c.lds_s, (j - A) * 1024, ls[j - A], in || c.live_s);
+      issue_atom_if(c.rb, c.lds_b, i * 1024, lb[i].offset, INTERIOR || lb[i & 1].chunk < c.valid);
+    } else if (C::RowsWave * 4 == C::Rows || C::RowsWave * wave < C::Rows) {
+      issue_atom_if(c.rs, c.lds_s, (j - A) * 1024, ls[j - A], INTERIOR || c.live_s);
     }
-  };
+  }
+  // The first quad's scales (into the first buffer) and the K tiles FROM .. TO-1 of the first S.
+  template <int FROM, int TO>
+  __device__ __forceinline__ void start() const {
+    if (FROM == 0) {
+      Copy c = tile(0, 0);
+      quad(c, 0);
+#pragma unroll
+      for (int j = A; j < A + SA; ++j) atom<false>(c, j);
+    }
+#pragma unroll
+    for (int t = FROM; t < TO; ++t) {
+      const Copy c = tile(t, t);
+#pragma unroll
+      for (int j = 0; j < A; ++j) atom<false>(c, j);
+    }
+  }
+};
 
+// acc += A·Bᵀ over one workgroup tile whose first copies are on their way (start()), and nothing
+// newer but what WAIT counts: the first barrier lets WAIT of the wave's memory operations be in
+// flight.  Schedule of the barrier ring, four K tiles (a quad) per iteration; the first two tiles of
+// a quad bring the next quad's scales along, half each, and k-step 1 reads the next tile's scales
+// next to its first fragments.  A barrier lets the code atoms of the S-2 tiles behind the awaited
+// one be in flight; scale atoms among them (a wave's own number) only make it wait for a few more
+// copies than it needs.
+template <class C, int S, int WAIT>
+__device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], const uint8_t* smem,
+                                         const Mx4Copies<C, S>& copies, int wave, int lane) {
+  using T = typename C::T;
+  using Copy = typename Mx4Copies<C, S>::Copy;
+  constexpr int FM = T::FM, A = T::Atoms, P = T::Products, R = T::Reads;
+  constexpr int SA = C::ScaleAtoms;
+  const int blocks = copies.box.blocks;
+  const int ktiles = blocks > 0 ? (blocks + 7) / 8 : 1;
+  const int pair = (0x2130 >> (4 * (lane >> 4))) & 15;  // 0, 3, 1, 2 (lane groups 0..3)
   const int wm = wave >> 1, wn = wave & 1;
   // Fragment rows start at multiples of 16, so the swizzle is the lane's own.
   const uint32_t lane_row = (uint32_t)(lane & 15) * 128u, swz = (lane >> 1) & 7;
@@ -179,7 +213,7 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
   // reads: products written as assembly must not follow a vector instruction that writes their
   // operand directly.
   auto mask_scales = [&](uint32_t (&s)[R], int kt) __attribute__((always_inline)) {
-    const int left = box.blocks - kt * 8 - 2 * pair;
+    const int left = blocks - kt * 8 - 2 * pair;
     const uint32_t keep = left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -197,7 +231,9 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
     constexpr int KK = decltype(kk)::value, S0 = decltype(s0)::value;
     constexpr int NA = KK == 1 ? A + decltype(ns)::value : 0;
     constexpr int H = P / (2 * (NA > 0 ? NA : 1));
-    auto go = [&](int j) __attribute__((always_inline)) { atom(c, j < A ? j : j + S0, interior); };
+    auto go = [&](int j) __attribute__((always_inline)) {
+      copies.template atom<decltype(interior)::value>(c, j < A ? j : j + S0);
+    };
 #pragma unroll
     for (int i = 0; i < P; ++i) {
 #pragma unroll
@@ -221,19 +257,7 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
 
   Mx4Frags f0, f1;
   uint32_t s0[R], s1[R];
-  {
-    Copy c = make_copy(0, 0);
-    scale_copy(c, 0);
-#pragma unroll
-    for (int j = A; j < A + SA; ++j) atom(c, j, std::false_type{});
-  }
-#pragma unroll
-  for (int t = 0; t < S; ++t) {
-    const Copy c = make_copy(t, t);
-#pragma unroll
-    for (int j = 0; j < A; ++j) atom(c, j, std::false_type{});
-  }
-  stage_barrier<A*(S - 1)>();  // the first quad's scales and tile 0 landed
+  stage_barrier<WAIT>();  // the first quad's scales and tile 0 landed
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     read(f0, smem, 0, r);
@@ -254,8 +278,8 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
     uint32_t (&sn)[R] = Q % 2 == 0 ? s1 : s0;
     step(f0, f1, s, sn, smem + cur * T::StageBytes, K0{}, Copy{}, Begin{}, Count{}, kt + 1, Next{}, interior);
     stage_barrier<A*(S - 2)>();  // tile kt+1 (and its scales) landed, stage `cur` free
-    Copy c = make_copy(kt + S, cur);
-    if (NS > 0) scale_copy(c, (kt >> 2) + 1);
+    Copy c = copies.tile(kt + S, cur);
+    if (NS > 0) copies.quad(c, (kt >> 2) + 1);
     step(f1, f0, s, sn, smem + nxt * T::StageBytes, K1{}, c, Begin{}, Count{}, kt + 1, Next{}, interior);
   };
   int kt = 0;
@@ -270,7 +294,35 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], uin
   stage_barrier<0>();
 }
 
-// C = alpha·A·Bᵀ + beta·C, or with offsets the same for the rows of each group with its own B.
+// The operands of tile t.
+template <class T>
+__device__ __forceinline__ Mx4Box mx4_box(const Mx4GemmParams& p, const RaggedTile& t) {
+  const int n0 = t.tn * T::BN;
+  Mx4Box b;
+  b.blocks = p.g.K / 32;
+  b.rows_a = t.rows;
+  b.rows_b = p.g.N - n0;
+  b.pitch_a = (uint32_t)p.g.lda;
+  b.pitch_b = (uint32_t)p.g.ldb;
+  b.pitch_as = (uint32_t)p.ld_as;
+  b.pitch_bs = (uint32_t)p.ld_bs;
+  b.ra = make_rsrc(p.g.A + (int64_t)t.row0 * p.g.lda, 0x7FFFFFFFull);
+  b.rb = make_rsrc(p.g.B + (int64_t)t.group * p.g.stride_b + (int64_t)n0 * p.g.ldb, 0x7FFFFFFFull);
+  b.ras = scale_rsrc(p.As + (int64_t)t.row0 * p.ld_as, p.ld_as, min(b.rows_a, T::BM), b.blocks);
+  b.rbs = scale_rsrc(p.Bs + (int64_t)t.group * p.stride_bs + (int64_t)n0 * p.ld_bs, p.ld_bs, min(b.rows_b, T::BN),
+                     b.blocks);
+  return b;
+}
+
+template <class T, int OUT, int SCALED, int PARK>
+__device__ __forceinline__ void mx4_store(const f32x4_t (&acc)[T::FN][T::FM], uint8_t* park, const Mx4GemmParams& p,
+                                          const RaggedTile& t, int wave, int lane) {
+  const GemmParams q = store_params(p.g.C, p.g.ldc, t.row0 + t.rows, p.g.N, p.g.vec_store, p.g.alpha, p.g.beta);
+  store_tile<T, OUT, SCALED, PARK>(acc, park, q, t.row0 + (wave >> 1) * T::TM, t.tn * T::BN + (wave & 1) * T::TN, lane);
+}
+
+// C = alpha·A·Bᵀ + beta·C, or with offsets the same for the rows of each group with its own B: one
+// tile per workgroup.
 template <int BM, int BN, int S, int OUT, int SCALED>
 __global__ void __launch_bounds__(kThreads, (Mx4Cfg<BM, BN, S>::MinBlocks)) gemm_mx4_kernel(Mx4GemmParams p) {
   using C = Mx4Cfg<BM, BN, S>;
@@ -288,25 +340,71 @@ __global__ void __launch_bounds__(kThreads, (Mx4Cfg<BM, BN, S>::MinBlocks)) gemm
     t.row0 = tm * BM;
     t.rows = p.g.rows - t.row0;
   }
-  const int n0 = t.tn * BN;
-  Mx4Box b;
-  b.blocks = p.g.K / 32;
-  b.rows_a = t.rows;
-  b.rows_b = p.g.N - n0;
-  b.pitch_a = (uint32_t)p.g.lda;
-  b.pitch_b = (uint32_t)p.g.ldb;
-  b.pitch_as = (uint32_t)p.ld_as;
-  b.pitch_bs = (uint32_t)p.ld_bs;
-  b.ra = make_rsrc(p.g.A + (int64_t)t.row0 * p.g.lda, 0x7FFFFFFFull);
-  b.rb = make_rsrc(p.g.B + (int64_t)t.group * p.g.stride_b + (int64_t)n0 * p.g.ldb, 0x7FFFFFFFull);
-  b.ras = scale_rsrc(p.As + (int64_t)t.row0 * p.ld_as, p.ld_as, min(b.rows_a, BM), b.blocks);
-  b.rbs = scale_rsrc(p.Bs + (int64_t)t.group * p.stride_bs + (int64_t)n0 * p.ld_bs, p.ld_bs, min(b.rows_b, BN), b.blocks);
+  Mx4Copies<C, S> copies;
+  copies.set(mx4_box<T>(p, t), smem, wave, lane);
+  copies.template start<0, S>();
   f32x4_t acc[T::FN][T::FM];
   zero_acc<T>(acc);
-  mx4_ring<C, S>(acc, smem, b, wave, lane);
-  const GemmParams q = store_params(p.g.C, p.g.ldc, t.row0 + t.rows, p.g.N, p.g.vec_store, p.g.alpha, p.g.beta);
-  store_tile<T, OUT, SCALED>(acc, smem + wave * (T::RingBytes / 4), q, t.row0 + (wave >> 1) * T::TM,
-                             n0 + (wave & 1) * T::TN, lane);
+  mx4_ring<C, S, T::Atoms*(S - 1)>(acc, smem, copies, wave, lane);
+  mx4_store<T, OUT, SCALED, T::RingBytes / 4>(acc, smem + wave * (T::RingBytes / 4), p, t, wave, lane);
+}
+
+// The same with a workgroup per CU that walks its XCD's tiles.  A 4-bit tile has a quarter of a
+// 16-bit one's K tiles, so what lies between the K loops weighs four times as much (of the 21 µs of
+// a tile with K = 2048: 1.0 to find it, 1.9 until its first K tile has landed, 4.4 to store it);
+// here the first K tile of the next tile is on its way while a tile is stored, from a park in the
+// second scale buffer (4 KiB a wave; the copies in flight go to the ring and the first).  Both first
+// K tiles ahead of the stores were 2-3 % slower on operands that come from HBM.  One tile per workgroup
+// and this, µs: 8192³ 222.3, 218.7; 4 groups of 2048 rows, N = 8192, K = 2048 101.4, 96.6, 32 of 256
+// 133.2, 125.2; 32 groups of 500 rows, N = 4096 101.9, 93.1, and level with B from HBM (107.5).
+template <int B, int S, int OUT, int SCALED>
+__global__ void __launch_bounds__(kThreads, 1) gemm_mx4_walk_kernel(Mx4GemmParams p) {
+  using C = Mx4Cfg<B, B, S>;
+  using T = typename C::T;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LdsBytes];
+  constexpr int Park = C::QuadBytes / 4;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RaggedPlan plan{};
+  if (p.g.offsets) plan = ragged_plan<B>(p.g.offsets, p.g.groups, p.g.rows, p.g.tiles_n);
+  else plan.tiles = p.g.tiles_m * p.g.tiles_n;
+  int first, count;
+  xcd_share(plan.tiles, blockIdx.x, first, count);
+  auto find = [&](int i, RaggedTile& t) __attribute__((always_inline)) {
+    if (p.g.offsets) {
+      ragged_find<B>(plan, p.g.offsets, p.g.groups, p.g.rows, p.g.tiles_n, p.g.group_m, first + i, t);
+    } else {
+      int tm;
+      band_tile(first + i, p.g.tiles_m, p.g.tiles_n, p.g.group_m, tm, t.tn);
+      t.group = 0;
+      t.row0 = tm * B;
+      t.rows = p.g.rows - t.row0;
+    }
+  };
+  int i = blockIdx.x >> 3;
+  if (i >= count) return;
+  RaggedTile t, next;
+  Mx4Copies<C, S> copies;
+  find(i, t);
+  copies.set(mx4_box<T>(p, t), smem, wave, lane);
+  copies.template start<0, 1>();
+  for (;;) {
+    copies.template start<1, S>();
+    i += gridDim.x >> 3;
+    const bool more = i < count;
+    if (more) find(i, next);
+    f32x4_t acc[T::FN][T::FM];
+    zero_acc<T>(acc);
+    mx4_ring<C, S, T::Atoms*(S - 1)>(acc, smem, copies, wave, lane);
+    if (more) {
+      copies.set(mx4_box<T>(p, next), smem, wave, lane);
+      copies.template start<0, 1>();
+    }
+    keep_acc<T>(acc);
+    mx4_store<T, OUT, SCALED, Park>(acc, smem + S * T::StageBytes + C::QuadBytes + wave * Park, p, t, wave, lane);
+    if (!more) return;
+    t = next;
+  }
 }
 
 }  // namespace tbg

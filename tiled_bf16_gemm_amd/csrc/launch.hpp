@@ -165,8 +165,9 @@ struct Mx4GemmParams {
   const uint8_t* Bs;
   int64_t ld_as, ld_bs, stride_bs;
 };
-// Tiles 256×256 and 128×128 (2 stages), 64×64 and 32×64 (2 or 4 stages).
-hipError_t launch_mx4_gemm(Mx4GemmParams p, int bm, int bn, int stages, int out_bf16, hipStream_t stream);
+// Tiles 256×256 (a workgroup for each of `cus` walks them) and 128×128 with 2 stages, 64×64 and 32×64
+// with 2 or 4.
+hipError_t launch_mx4_gemm(Mx4GemmParams p, int bm, int bn, int stages, int out_bf16, int cus, hipStream_t stream);
 // Products with few rows (gemm_rows.hpp), B stored N×K, at most 16 rows when dense; fmt 0 bf16, 1
 // fp16 (A, B and their pitches as GroupedParams), 2 microscaled 4-bit; out as launch_grouped.
 hipError_t launch_few_rows(Mx4GemmParams p, int fmt, int out, hipStream_t stream);

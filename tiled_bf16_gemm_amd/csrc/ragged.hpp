@@ -57,30 +57,37 @@ struct RaggedTile {
   int tn;    // tile column
 };
 
-// The tile of workgroup `bid`, BM rows high, of `tiles_n` tile columns; false when there is none
-// (the grid is an upper bound).  Workgroups are dealt round-robin to the 8 XCDs, so XCD x gets
-// the x-th eighth of the tiles that exist, in order: groups one after another, inside a group
-// in band_tile's, which keeps a group's operands in few L2 caches.
+// Tiles of BM rows over the groups, and each lane's share of them.
+struct RaggedPlan {
+  int upto, mine;  // tile rows up to and with this lane's groups; in them
+  int begin, end;  // the rows of this lane's group (up to 64 groups)
+  int tiles;       // tiles of all groups
+};
+
 template <int BM>
-__device__ __forceinline__ bool ragged_tile(const int32_t* offsets, int groups, int rows, int tiles_n, int height,
-                                            int bid, RaggedTile& t) {
-  const int lane = threadIdx.x & 63;
-  const int per = (groups + 63) >> 6, g0 = lane * per;
-  int mine = 0, begin = 0, end = 0;
+__device__ __forceinline__ RaggedPlan ragged_plan(const int32_t* offsets, int groups, int rows, int tiles_n) {
+  const int per = (groups + 63) >> 6, g0 = (threadIdx.x & 63) * per;
+  RaggedPlan p;
+  p.mine = p.begin = p.end = 0;
   for (int j = 0; j < per; ++j) {
     if (g0 + j < groups) {
-      group_rows(offsets, g0 + j, rows, begin, end);
-      mine += (end - begin + BM - 1) / BM;
+      group_rows(offsets, g0 + j, rows, p.begin, p.end);
+      p.mine += (p.end - p.begin + BM - 1) / BM;
     }
   }
-  const int upto = wave_prefix_sum(mine);
-  const int total = __builtin_amdgcn_readlane(upto, 63) * tiles_n;
-  const int q = total >> 3, r = total & 7, x = bid & 7, i = bid >> 3;
-  if (i >= (x < r ? q + 1 : q)) return false;
-  const int lid = x < r ? x * (q + 1) + i : r * (q + 1) + (x - r) * q + i;
+  p.upto = wave_prefix_sum(p.mine);
+  p.tiles = __builtin_amdgcn_readlane(p.upto, 63) * tiles_n;
+  return p;
+}
 
-  int at = (upto - mine) * tiles_n;  // this lane's first tile
-  int found = -1, fb = 0, fe = 0, fi = 0;
+// Tile number `lid` (below plan.tiles): groups one after another, inside a group in band_tile's
+// order, which keeps a group's operands in few L2 caches.
+template <int BM>
+__device__ __forceinline__ void ragged_find(const RaggedPlan& p, const int32_t* offsets, int groups, int rows,
+                                            int tiles_n, int height, int lid, RaggedTile& t) {
+  const int per = (groups + 63) >> 6, g0 = (threadIdx.x & 63) * per;
+  int at = (p.upto - p.mine) * tiles_n;  // this lane's first tile
+  int found = -1, fb = 0, fe = 0, fi = 0, begin = p.begin, end = p.end;
   for (int j = 0; j < per; ++j) {
     if (g0 + j < groups) {
       if (per > 1) group_rows(offsets, g0 + j, rows, begin, end);
@@ -97,11 +104,29 @@ __device__ __forceinline__ bool ragged_tile(const int32_t* offsets, int groups, 
   const int src = __builtin_ctzll(__ballot(found >= 0));
   t.group = __builtin_amdgcn_readlane(found, src);
   const int b = __builtin_amdgcn_readlane(fb, src), e = __builtin_amdgcn_readlane(fe, src);
-  const int in_group = __builtin_amdgcn_readlane(fi, src);
   int tm;
-  band_tile(in_group, (e - b + BM - 1) / BM, tiles_n, height, tm, t.tn);
+  band_tile(__builtin_amdgcn_readlane(fi, src), (e - b + BM - 1) / BM, tiles_n, height, tm, t.tn);
   t.row0 = b + tm * BM;
   t.rows = e - t.row0;
+}
+
+// Workgroups are dealt round-robin to the 8 XCDs: XCD x takes the x-th eighth of `tiles`, and
+// workgroup `bid` is the (bid / 8)-th on it.  Its XCD's first tile and number of tiles.
+__device__ __forceinline__ void xcd_share(int tiles, int bid, int& first, int& count) {
+  const int q = tiles >> 3, r = tiles & 7, x = bid & 7;
+  count = x < r ? q + 1 : q;
+  first = x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q;
+}
+
+// The tile of workgroup `bid`, one tile each; false when there is none (the grid is an upper bound).
+template <int BM>
+__device__ __forceinline__ bool ragged_tile(const int32_t* offsets, int groups, int rows, int tiles_n, int height,
+                                            int bid, RaggedTile& t) {
+  const RaggedPlan p = ragged_plan<BM>(offsets, groups, rows, tiles_n);
+  int first, count;
+  xcd_share(p.tiles, bid, first, count);
+  if ((bid >> 3) >= count) return false;
+  ragged_find<BM>(p, offsets, groups, rows, tiles_n, height, first + (bid >> 3), t);
   return true;
 }
 
