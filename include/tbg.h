@@ -444,7 +444,7 @@ tbg_status tbg_conv2d_fwd(const tbg_conv2d_shape* shape, float alpha, const void
  *             They are read on `stream` when the work runs, so a captured graph replays with the
  *             offsets then in memory.  Values outside 0..M are taken as the nearer bound and a
  *             descending pair as an empty group: nothing outside the operands is read or written
- *             (but rows that two groups then share hold either's result).
+ *             (but what C then holds in rows that several groups claim is not specified).
  * Limits: M, N and K (P and Q) up to 2^30, groups up to 4096, leading dimensions of 16-bit
  * operands below 2^22 elements. */
 
@@ -509,7 +509,8 @@ tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t 
  * alignment of whole elements) to rows of K = cols rounded up to 32 columns; the columns past cols
  * are zeros.  Per block, with m the largest magnitude: scale exponent clamp(floor(log2 m) - 2,
  * -127, 127), codes rounded to nearest even and clipped to magnitude 6.  A block that holds a NaN
- * or an infinity gets scale byte 255 and zero codes.  rows == 0 or cols == 0 is a no-op.
+ * or an infinity gets scale byte 255 and zero codes.  X, codes and scales must not overlap.
+ * rows == 0 or cols == 0 is a no-op.
  * Returns INVALID_VALUE (negative sizes, pitches too small, null pointers, type), MISALIGNED (X off
  * its element size; codes, scales or their pitches off 16), UNSUPPORTED (cols above 2^30),
  * NO_DEVICE / HIP. */

@@ -377,6 +377,31 @@ def test_grouped_product_exact(case):
 
 
 @gpu
+@pytest.mark.parametrize("groups,M", [(40, 320), (40, 7600)])
+def test_offsets_that_descend_stay_inside_the_operands(groups, M):
+    """Every second pair spans all rows, the others descend: each row of C comes from one of the groups,
+    and nothing else is written (7600 rows: the walking tile; 320: 32-row tiles)."""
+    N, K = 300, 96
+    print(f"mx4 descending offsets groups={groups} M={M}", flush=True)
+    rng = np.random.default_rng(M)
+    a, sa, va = _random_mx4(rng, (M,), K)
+    b, sb, vb = _random_mx4(rng, (groups, N), K, pitch_codes=16)
+    off = torch.tensor([0, M] * (groups // 2) + [0], dtype=torch.int32, device="cuda")
+    out = torch.full((M + 2, N), 7.0, device="cuda")
+    _ops().mx4_gemm_grouped(a, sa, b, sb, off, "f32", out=out[1:M + 1])
+    assert (out[0] == 7).all() and (out[M + 1] == 7).all()
+    ours = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    for e in range(groups):
+        ours |= out[1:M + 1] == (va @ vb[e].t().contiguous()).float()
+    assert ours.all()
+    off = torch.tensor([-3, 5, 1 << 30] + [5] * (groups - 2), dtype=torch.int32, device="cuda")
+    _ops().mx4_gemm_grouped(a, sa, b, sb, off, "f32", out=out[1:M + 1])
+    assert (out[0] == 7).all() and (out[M + 1] == 7).all()
+    assert torch.equal(out[1:6].double(), va[:5] @ vb[0].t().contiguous())
+    assert torch.equal(out[6:M + 1].double(), va[5:] @ vb[1].t().contiguous())
+
+
+@gpu
 @pytest.mark.parametrize("M", [9, 600])
 def test_product_offsets_past_32_bits(M):
     """Codes at nearly the largest pitch (600 rows of 8 MiB) and matrices 4 GiB apart, scales too."""

@@ -106,15 +106,17 @@ tbg_status check_workspace(size_t need, const void* workspace, size_t have) {
 // A round of tiles, one on every slot the chip has for them, takes about `fixed` µs to start and to
 // store and `per` µs for each K tile (128 bytes of a row); the smaller tiles share a CU, and a
 // round that does not fill costs them only `part` of one, since the next tiles start as others end.
-// Measured on MI355X over 8 to 64 groups, K of 300 to 4096 (µs, chosen first): 8 groups of 2048
-// rows, N = 1024, K = 512 26 (128) against 36 (256); 8 of 1024 rows, N = 1024, K = 4096 73 (256)
-// against 91 (128); 100 of 30 rows, N = 700, K = 600 55 (64) against 59 (128).
+// The figures are fitted to every tile's time on thousands of shapes (MI355X, 4 to 64 groups of 70 to
+// 2048 rows on average, N of 256 to 14336, K of 256 to 8192; the 4-bit ones also dense): the tile
+// chosen takes 1.0 % (16-bit rows), 1.4 % (weight gradient) and 0.9 % (4 bits) longer than the
+// best one on average.
 struct TileTime {
   int b, per_cu;
   double fixed, per, part;
 };
-const TileTime kTiles16[] = {{256, 1, 6.5, 1.25, 1.0}, {128, 2, 5.0, 1.05, 0.25}, {64, 3, 4.0, 0.75, 0.2}};
-const TileTime kTiles4[] = {{256, 1, 6.5, 1.7, 1.0}, {128, 2, 5.0, 1.2, 0.25}, {64, 2, 4.0, 0.37, 0.2}};
+const TileTime kTilesRows[] = {{256, 1, 9.2, 0.98, 1.0}, {128, 2, 3.65, 0.97, 0.13}, {64, 3, 2.3, 0.61, 0.58}};
+const TileTime kTilesGrad[] = {{256, 1, 14.2, 0.88, 1.0}, {128, 2, 4.1, 1.05, 0.1}, {64, 3, 4.6, 0.52, 0.45}};
+const TileTime kTiles4[] = {{256, 1, 10.5, 0.98, 1.0}, {128, 2, 4.1, 1.05, 0.135}, {64, 2, 4.2, 0.42, 0.63}};
 
 double tile_time(const TileTime& t, double tiles, double ktiles, int cus) {
   double rounds = tiles / ((double)t.per_cu * cus);
@@ -125,16 +127,16 @@ double tile_time(const TileTime& t, double tiles, double ktiles, int cus) {
 }
 
 // The tile for `groups` groups that share `rows` rows.  How the rows split is not known here:
-// groups of the average size are assumed, each ending half way into its last tile.  Up to 64 (160)
+// groups of the average size are assumed, each ending half way into its last tile.  Up to 64 (128)
 // rows a group the product is bound by the bytes of B, which a tile of 64 (128) rows reads as
-// well with less of it masked (64 groups, N = K = 2048: 64 rows 130 µs with 64-row tiles, 153 with
-// 128; 128 rows 159 µs with 128, 182 with 256).
+// well with less of it masked (64 groups, N = K = 2048, 16 bits: 64 rows 130 µs with 64-row tiles,
+// 153 with 128; 128 rows 159 µs with 128, 182 with 256).
 int choose_rows_tile(const TileTime (&t)[3], double groups, double rows, int64_t N, double ktiles, int cus) {
   const double average = rows / groups;
   int best = 64;
   double best_time = 0;
   for (const TileTime& c : t) {
-    if ((c.b > 64 && average <= 64) || (c.b > 128 && average <= 160)) continue;
+    if ((c.b > 64 && average <= 64) || (c.b > 128 && average <= 128)) continue;
     const double per = groups > 1 ? average / c.b + 0.5 : ceil(average / c.b);
     const double tiles = groups * (per > 1 ? per : 1) * (double)((N + c.b - 1) / c.b);
     const double time = tile_time(c, tiles, ktiles, cus);
@@ -209,7 +211,7 @@ tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   st = check_device(&cus);
   if (st != TBG_OK) return st;
   const double active = (double)(groups < M ? groups : M);
-  const int b = choose_rows_tile(kTiles16, active, (double)M, N, ceil(K / 64.0), cus);
+  const int b = choose_rows_tile(kTilesRows, active, (double)M, N, ceil(K / 64.0), cus);
   const bool few = nk && takes_few_rows(active, (double)M, N, cus);
   hipStream_t s = (hipStream_t)stream;
   uint8_t* const area = tbg::repack_area(workspace, workspace_bytes, ra.bytes + rb.bytes);
@@ -301,7 +303,7 @@ tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t 
   // Every group has the same tiles, its rows are the sum's terms.
   int b = 0;
   double best = 0;
-  for (const TileTime& t : kTiles16) {
+  for (const TileTime& t : kTilesGrad) {
     const double tiles = (double)groups * (double)((P + t.b - 1) / t.b) * (double)((Q + t.b - 1) / t.b);
     const double time = tile_time(t, tiles, ceil((double)M / (double)groups / 64), cus);
     if (!b || time < best) {

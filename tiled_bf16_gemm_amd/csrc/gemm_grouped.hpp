@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, (RingCfg<BM, BN, S>::MinBlocks)) gem
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RaggedTile t;
-  if (!ragged_tile<BM>(p.offsets, p.groups, p.rows, p.tiles_n, p.group_m, blockIdx.x, t)) return;
+  if (!ragged_tile<BM>(p, p.group_m, blockIdx.x, t)) return;
   const int n0 = t.tn * BN;
   const uint8_t* b = p.B + (int64_t)t.group * p.stride_b + (BL == kSumInner ? (int64_t)n0 * p.ldb : (int64_t)n0 * 2);
   const TileBox ba = make_box<kSumInner>(p.A + (int64_t)t.row0 * p.lda, (uint32_t)p.lda, t.rows, p.K);

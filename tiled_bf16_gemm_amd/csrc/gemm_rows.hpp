@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(64 * kRowsWaves) gemm_rows_kernel(Mx4GemmParam
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RaggedTile t;
   if (g.offsets) {
-    if (!ragged_tile<16>(g.offsets, g.groups, g.rows, g.tiles_n, 1, blockIdx.x, t)) return;
+    if (!ragged_tile<16>(g, 1, blockIdx.x, t)) return;
   } else {  // at most 16 rows
     t.group = 0;
     t.row0 = 0;

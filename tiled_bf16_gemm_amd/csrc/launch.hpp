@@ -126,7 +126,7 @@ struct GroupedParams {
   int64_t lda, ldb, stride_b, ldc, stride_c;
   int groups, rows;
   int M, N, K;
-  int tiles_m, tiles_n, group_m;
+  int tiles_m, tiles_n, group_m;  // rows product over offsets: tiles_m bounds all groups' tile rows
   int per_xcd;     // weight gradient: consecutive tiles of a group per XCD
   int by_rows;     // weight gradient: the groups run in the order of their rows (at most 64 groups)
   int vec_store;
@@ -137,6 +137,8 @@ struct GroupedParams {
 // 256×256, 128×128, 64×64; they fill the tile counts and the grid.
 hipError_t launch_grouped(GroupedParams p, int bm, int bn, int in, int b_layout, int out, hipStream_t stream);
 hipError_t launch_wgrad(GroupedParams p, int bm, int bn, int in, int out, hipStream_t stream);
+// Workgroups one launch takes: it counts its threads (256 a workgroup) in 32 bits.
+constexpr int64_t kMaxGrid = (1 << 24) - 1;
 // Upper bound of the tiles of height bm over any split of `rows` rows into `groups` groups.
 inline int64_t ragged_tiles_bound(int64_t rows, int64_t groups, int64_t bm) {
   const int64_t g = groups < rows ? groups : rows;

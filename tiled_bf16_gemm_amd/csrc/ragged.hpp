@@ -4,12 +4,14 @@
 // Group e holds rows offsets[e] .. offsets[e+1]-1.  The offsets stay in device memory (a router
 // writes them there, and a captured graph replays with new ones), so the host only knows the
 // number of rows and of groups: it launches as many workgroups as the worst split needs
-// (ragged_grid) and each workgroup finds its tile from the offsets, every wave for itself: a lane
-// counts the tiles of its share of the groups, one prefix sum over the lanes places them, and
+// (ragged_tiles_bound) and each workgroup finds its tile from the offsets, every wave for itself: a
+// lane counts the tiles of its share of the groups, one prefix sum over the lanes places them, and
 // the lane whose range holds the workgroup's number answers.  That is one dependent load and ≈30
 // vector instructions before the K loop, against a launch of its own (and a table in a workspace)
 // for a planning kernel.  Offsets are clamped to the rows that exist and to ascending pairs, so
-// no value in them takes an access outside the operands.
+// no value in them takes an access outside the operands; offsets that descend make no more tiles
+// than any others can (tile_rows bounds them: their sum might even pass 32 bits, but the first lane
+// that covers a tile below the bound has not wrapped).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -65,7 +67,8 @@ struct RaggedPlan {
 };
 
 template <int BM>
-__device__ __forceinline__ RaggedPlan ragged_plan(const int32_t* offsets, int groups, int rows, int tiles_n) {
+__device__ __forceinline__ RaggedPlan ragged_plan(const int32_t* offsets, int groups, int rows, int tile_rows,
+                                                  int tiles_n) {
   const int per = (groups + 63) >> 6, g0 = (threadIdx.x & 63) * per;
   RaggedPlan p;
   p.mine = p.begin = p.end = 0;
@@ -76,7 +79,7 @@ __device__ __forceinline__ RaggedPlan ragged_plan(const int32_t* offsets, int gr
     }
   }
   p.upto = wave_prefix_sum(p.mine);
-  p.tiles = __builtin_amdgcn_readlane(p.upto, 63) * tiles_n;
+  p.tiles = min(__builtin_amdgcn_readlane(p.upto, 63) * tiles_n, tile_rows * tiles_n);
   return p;
 }
 
@@ -120,13 +123,12 @@ __device__ __forceinline__ void xcd_share(int tiles, int bid, int& first, int& c
 
 // The tile of workgroup `bid`, one tile each; false when there is none (the grid is an upper bound).
 template <int BM>
-__device__ __forceinline__ bool ragged_tile(const int32_t* offsets, int groups, int rows, int tiles_n, int height,
-                                            int bid, RaggedTile& t) {
-  const RaggedPlan p = ragged_plan<BM>(offsets, groups, rows, tiles_n);
+__device__ __forceinline__ bool ragged_tile(const GroupedParams& g, int height, int bid, RaggedTile& t) {
+  const RaggedPlan p = ragged_plan<BM>(g.offsets, g.groups, g.rows, g.tiles_m, g.tiles_n);
   int first, count;
   xcd_share(p.tiles, bid, first, count);
   if ((bid >> 3) >= count) return false;
-  ragged_find<BM>(p, offsets, groups, rows, tiles_n, height, first + (bid >> 3), t);
+  ragged_find<BM>(p, g.offsets, g.groups, g.rows, g.tiles_n, height, first + (bid >> 3), t);
   return true;
 }
 
