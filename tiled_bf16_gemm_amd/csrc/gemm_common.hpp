@@ -294,9 +294,10 @@ __device__ __forceinline__ typename Half4<OUT>::vec round4(const f32x4_t& v) {
 // wave parks its block (in one or two bands of rows) in its own quarter of the now idle ring,
 // then reads it back as 16-byte pieces of whole rows, so every store instruction writes whole
 // row segments.  Whole-row stores are non-temporal: C is written once and not read again here,
-// so it should not push operand tiles out of the caches.  OUT: 0 fp32, 1 bf16, 2 fp16.  With SCALED the park keeps the fp32
-// sums and each piece becomes alpha·S + beta·C_old (C_old read only when beta != 0) before it is
-// rounded to C's type ("GEMM" page, tensor-core section: C <- alpha·A·B + beta·C).
+// so it should not push operand tiles out of the caches.  OUT: 0 fp32, 1 bf16, 2 fp16.  With SCALED
+// the park keeps the fp32 sums and each piece becomes alpha·S + beta·C_old (C_old read only when
+// beta != 0) before it is rounded to C's type ("GEMM" page, tensor-core section: C <- alpha·A·B +
+// beta·C).
 // PARK: bytes of LDS the wave parks in (a quarter of the ring; less splits the block into more bands of
 // rows, and into column parts where 16 whole rows do not fit).
 template <class T, int OUT, int SCALED, int PARK = T::RingBytes / 4>

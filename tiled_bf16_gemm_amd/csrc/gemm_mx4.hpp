@@ -9,9 +9,9 @@
 //    quad), 32 rows per copy atom, two buffers of 32 bytes a row (256×256: 4 atoms per wave and
 //    quad next to 64 atoms of codes; the ring and the buffers are the whole 160 KiB of LDS).  Copies
 //    of 16 bytes per row, for two K tiles, took as many atoms but twice the cache lines (8192³
-//    241 against 234 µs, 2048³ 11.4 against 11.0).  Both 16-byte halves of rows 8..15 of 16 are exchanged in LDS, so that a
-//    fragment's 16 rows, 32 bytes apart, are read from distinct banks.  The instruction takes a lane's
-//    scale from one byte of a register, chosen by an immediate.
+//    241 against 234 µs, 2048³ 11.4 against 11.0).  The two 16-byte halves of rows 8..15 of 16 are
+//    exchanged in LDS, so that a fragment's 16 rows, 32 bytes apart, are read from distinct banks.  The
+//    instruction takes a lane's scale from one byte of a register, chosen by an immediate.
 //  * Placement.  Lane l multiplies row l%16 and, in k-step kk, block 2·pair(l/16)+kk of the tile
 //    (not 4kk + l/16): its two k-steps then need two neighbouring scale bytes, one 16-bit LDS read
 //    per fragment and K tile.  The sum runs over the tile's blocks in another order, the same for A

@@ -141,8 +141,8 @@ struct GradTile {
 // Every group has the same tiles but its own number of rows, and so its own cost per tile.  Each
 // XCD takes an eighth of every group's tiles (p.per_xcd consecutive ones, column-major within
 // bands of tile rows, so that they share operand rows in its L2), so the XCDs stay level however
-// the rows are split; and (p.by_rows, up to 64 groups) they run in the order of their rows, the longest first, so
-// that the last workgroups to start are the short ones.  (One contiguous eighth of all tiles per
+// the rows are split; and (p.by_rows, up to 64 groups) they run in the order of their rows, the
+// longest first, so that the last workgroups to start are the short ones.  (One contiguous eighth of all tiles per
 // XCD, as the products of equal tiles use, left the XCD of the longest group running alone: 381 µs
 // against 248 for 8 groups of 16384 rows in all, 4096×2048.)
 __device__ __forceinline__ bool grad_tile(const GroupedParams& p, int bid, GradTile& t) {
