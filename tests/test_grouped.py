@@ -284,6 +284,56 @@ def test_rows_alpha_beta(dtype, out_dtype):
     assert (out[inside] == 6).all() and (out[edges[-1]:] == 3).all()
 
 
+# Sizes that take the 256×256 tile (test_grouped_handoff.py checks the choice for the same sizes):
+# several tiles a group, overhang on every side, a group without rows and one of one row past a tile.
+LARGE_ROWS = ([1200, 0, 800, 257, 1743], 2, 7, 3402, 1276)
+LARGE_GRAD = ([1200, 0, 1800, 257, 2743], 1, 2, 2003, 2058)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_rows_exact_on_the_large_tile(layout, dtype):
+    sizes, before, behind, N, K = LARGE_ROWS
+    edges, G, dt = _offsets(sizes, before), len(sizes), TORCH[dtype]
+    M = edges[-1] + behind
+    print(f"rows {dtype} {layout} groups={G} M={M} N={N} K={K}", flush=True)
+    gen = _gen(70)
+    A, B = _ints(gen, (M, K), dt), _ints(gen, (G, K, N) if layout == "kn" else (G, N, K), dt)
+    want = _ref_rows(A, B, edges, layout)
+    A[:before], A[edges[-1]:], B[1] = float("nan"), float("nan"), float("nan")
+    inside = slice(before, edges[-1])
+    for out_dtype in ("f32", dtype):
+        out = torch.full((M, N), -77.0, dtype=TORCH[out_dtype], device="cuda")
+        _ops().gemm_grouped(A, B, _dev(edges), layout, out_dtype, out=out)
+        assert torch.equal(out[inside], want[inside].to(out.dtype)), out_dtype
+        assert (out[:before] == -77).all() and (out[edges[-1]:] == -77).all()
+    out.fill_(2.0)
+    _ops().gemm_grouped(A, B, _dev(edges), layout, dtype, out=out, alpha=2.0, beta=-3.0)
+    assert torch.equal(out[inside], (2 * want[inside] - 6).to(dt))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_wgrad_exact_on_the_large_tile(dtype):
+    sizes, before, behind, P, Q = LARGE_GRAD
+    edges, G, dt = _offsets(sizes, before), len(sizes), TORCH[dtype]
+    M = edges[-1] + behind
+    print(f"wgrad {dtype} groups={G} M={M} P={P} Q={Q}", flush=True)
+    gen = _gen(71)
+    X, Y = _ints(gen, (M, P), dt), _ints(gen, (M, Q), dt)
+    want = _ref_wgrad(X, Y, edges)
+    for t in (X, Y):
+        t[:before], t[edges[-1]:] = float("nan"), float("nan")
+    for out_dtype in ("f32", dtype):
+        out = torch.full((G, P, Q), float("nan"), dtype=TORCH[out_dtype], device="cuda")
+        _ops().gemm_grouped_wgrad(X, Y, _dev(edges), out_dtype, out=out)
+        assert torch.equal(out, want.to(out.dtype)), out_dtype
+    out.fill_(4.0)
+    _ops().gemm_grouped_wgrad(X, Y, _dev(edges), dtype, out=out, alpha=0.5, beta=1.0)
+    assert torch.equal(out, (0.5 * want + 4).to(dt))
+
+
 @gpu
 def test_rows_infinities_stay_in_their_group():
     edges, N, K, dt = _offsets([10, 20, 30], 0), 40, 48, torch.bfloat16

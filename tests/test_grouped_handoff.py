@@ -31,6 +31,13 @@ CASES = [
     ("mx4", dict(M=50, N=70000, K=1056), "ring 64x64, 2 stages"),
     ("mx4", dict(M=2000, N=2000, K=2080), "ring 128x128, 2 stages"),
     ("mx4", dict(M=4000, N=4000, K=4128), "ring 256x256, 2 stages"),
+    # the sizes of the exact tests of the large tiles
+    ("grouped", dict(groups=5, M=4009, N=3402, K=1276, layout="nk"), "ring 256x256"),
+    ("grouped", dict(groups=5, M=4009, N=3402, K=1276, layout="kn"), "ring 256x256"),
+    ("wgrad", dict(groups=5, M=6003, P=2003, Q=2058), "ring 256x256"),
+    ("mx4", dict(M=5100, N=5003, K=2080), "ring 256x256, 2 stages"),
+    ("mx4_grouped", dict(groups=5, M=6009, N=4603, K=2080), "ring 256x256, 2 stages"),
+    ("mx4_grouped", dict(groups=4, M=8000, N=5003, K=2080), "ring 256x256, 2 stages"),
 ]
 
 
@@ -42,8 +49,8 @@ def _child():
     from tiled_bf16_gemm_amd import torch_ops as ops
     product, check = tbg._lib, ctypes.CDLL(CHECK_LIB)
     for n in ("tbg_gemm_grouped", "tbg_gemm_grouped_workspace_query", "tbg_gemm_grouped_wgrad",
-              "tbg_gemm_grouped_wgrad_workspace_query", "tbg_mx4_gemm", "tbg_mx4_quantize", "tbg_status_string",
-              "tbg_last_error"):
+              "tbg_gemm_grouped_wgrad_workspace_query", "tbg_mx4_gemm", "tbg_mx4_gemm_grouped", "tbg_mx4_quantize",
+              "tbg_status_string", "tbg_last_error"):
         f, g = getattr(check, n), getattr(product, n)
         f.restype, f.argtypes = g.restype, g.argtypes
     gen = torch.Generator(device="cuda").manual_seed(1)
@@ -58,6 +65,14 @@ def _child():
 
             def run():
                 return ops.mx4_gemm(a, sa, b, sb, "f32")
+        elif call == "mx4_grouped":
+            edges = [e * c["M"] // c["groups"] for e in range(c["groups"])] + [c["M"]]
+            off = torch.tensor(edges, dtype=torch.int32, device="cuda")
+            a, sa = ops.mx4_quantize(randn(c["M"], c["K"]))
+            b, sb = ops.mx4_quantize(randn(c["groups"], c["N"], c["K"]))
+
+            def run():
+                return ops.mx4_gemm_grouped(a, sa, b, sb, off, "f32")
         else:
             edges = [e * c["M"] // c["groups"] for e in range(c["groups"])] + [c["M"] - 1]
             off = torch.tensor(edges, dtype=torch.int32, device="cuda")

@@ -270,7 +270,7 @@ def _random_mx4(rng, shape, K, spread=1, pitch_codes=0, pitch_scales=16):
 # one row; one block; K ends inside a tile of 256, of 512; sizes that overhang and take each tile
 PRODUCTS = [(1, 1, 32), (1, 16, 64), (1, 300, 1024), (3, 40, 288), (16, 130, 224), (17, 70, 256), (64, 64, 512),
             (33, 129, 544), (65, 200, 736), (200, 520, 320), (300, 1030, 800), (1030, 2050, 96), (2100, 2056, 288),
-            (4100, 4100, 160)]
+            (4100, 4100, 160), (20, 70001, 96), (50, 70001, 288)]
 
 
 @gpu
@@ -377,11 +377,10 @@ def test_grouped_product_exact(case):
 
 
 @gpu
-@pytest.mark.parametrize("groups,M", [(40, 320), (40, 7600)])
-def test_offsets_that_descend_stay_inside_the_operands(groups, M):
+@pytest.mark.parametrize("groups,M,N,K", [(40, 320, 300, 96), (4, 8000, 5003, 2080)])
+def test_offsets_that_descend_stay_inside_the_operands(groups, M, N, K):
     """Every second pair spans all rows, the others descend: each row of C comes from one of the groups,
-    and nothing else is written (7600 rows: the walking tile; 320: 32-row tiles)."""
-    N, K = 300, 96
+    and nothing else is written (8000 rows: the walking tile; 320: 32-row tiles)."""
     print(f"mx4 descending offsets groups={groups} M={M}", flush=True)
     rng = np.random.default_rng(M)
     a, sa, va = _random_mx4(rng, (M,), K)
@@ -399,6 +398,60 @@ def test_offsets_that_descend_stay_inside_the_operands(groups, M):
     assert (out[0] == 7).all() and (out[M + 1] == 7).all()
     assert torch.equal(out[1:6].double(), va[:5] @ vb[0].t().contiguous())
     assert torch.equal(out[6:M + 1].double(), va[5:] @ vb[1].t().contiguous())
+
+
+# Sizes that take the 256×256 tile with more tiles than compute units, so that workgroups walk from
+# tile to tile (test_grouped_handoff.py checks the choice): an odd pitch of C, overhang, a tail in K.
+@gpu
+def test_walking_tile_exact():
+    M, N, K = 5100, 5003, 2080
+    print(f"mx4 product M={M} N={N} K={K}", flush=True)
+    rng = np.random.default_rng(81)
+    a, sa, va = _random_mx4(rng, (M,), K, pitch_codes=16)
+    b, sb, vb = _random_mx4(rng, (N,), K)
+    want = va @ vb.t().contiguous()
+    for out_dtype, pad in (("f32", 1), ("bf16", 0), ("bf16", 1)):
+        full = torch.full((M + 1, N + pad), -9.0, dtype=TORCH[out_dtype], device="cuda")
+        _ops().mx4_gemm(a, sa, b, sb, out_dtype, out=full[:M, :N])
+        assert torch.equal(full[:M, :N], want.to(full.dtype)), out_dtype
+        assert (full[M] == -9).all() and (full[:, N:] == -9).all()
+    for out_dtype in ("f32", "bf16"):
+        out = torch.full((M, N), 3.0, dtype=TORCH[out_dtype], device="cuda")
+        _ops().mx4_gemm(a, sa, b, sb, out_dtype, out=out, alpha=0.5, beta=2.0)
+        assert torch.equal(out, (0.5 * want + 6).to(out.dtype))
+
+
+@gpu
+def test_walking_tile_over_groups_and_replays():
+    """The ragged product on the walking tile, eager and replayed with other offsets in place."""
+    sizes, N, K = ([2500, 0, 1990, 257, 1253], [0, 1, 5400, 0, 599], [1200] * 5), 4603, 2080
+    M, G = 6009, 5
+    print(f"mx4 grouped product groups={G} M={M} N={N} K={K}", flush=True)
+    rng = np.random.default_rng(82)
+    a, sa, va = _random_mx4(rng, (M,), K)
+    b, sb, vb = _random_mx4(rng, (G, N), K)
+    want, edges = [], []
+    for s in sizes:
+        edges.append([3] + [3 + int(v) for v in np.cumsum(s)])
+        w = torch.full((M, N), 5.0, dtype=torch.float64, device="cuda")
+        for e in range(G):
+            w[edges[-1][e]:edges[-1][e + 1]] = va[edges[-1][e]:edges[-1][e + 1]] @ vb[e].t().contiguous()
+        want.append(w)
+    off = torch.tensor(edges[0], dtype=torch.int32, device="cuda")
+    out = torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    _ops().mx4_gemm_grouped(a, sa, b, sb, off, "bf16", out=out)
+    assert torch.equal(out, want[0].to(out.dtype))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _ops().mx4_gemm_grouped(a, sa, b, sb, off, "bf16", out=out)
+    for i in (1, 2, 0, 1):
+        off.copy_(torch.tensor(edges[i], dtype=torch.int32))
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i].to(out.dtype)), i
+        eager = _ops().mx4_gemm_grouped(a, sa, b, sb, off, "f32", out=torch.full((M, N), 5.0, device="cuda"))
+        assert torch.equal(eager, want[i].float()), i
 
 
 @gpu
