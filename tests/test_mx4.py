@@ -161,6 +161,14 @@ def test_grouped_product_refusals(over, status):
     assert e.value.status == status, e.value
 
 
+@pytest.mark.gpu
+def test_more_tiles_than_a_launch_takes_are_refused():
+    """2^24 workgroups of 64 columns: refused on the host, nothing is launched."""
+    with pytest.raises(tbg.Error) as e:
+        tbg.mx4_gemm(**_p(M=1, N=1 << 30, K=32, lda=16, ldb=16, ldc=1 << 30))
+    assert e.value.status == tbg.ERR_UNSUPPORTED, e.value
+
+
 def test_empty_calls_need_no_device():
     tbg.mx4_quantize(**_q(rows=0, X=0, codes=0, scales=0))
     tbg.mx4_dequantize(**_q(cols=0, X=0, codes=0, scales=0))

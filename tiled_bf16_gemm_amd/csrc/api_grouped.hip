@@ -158,6 +158,12 @@ bool takes_few_rows(double groups, double rows, int64_t N, int cus) {
 
 bool too_many_tiles(int64_t tiles) { return tiles > INT32_MAX - 8; }
 
+tbg_status launch_status(const char* what, hipError_t e) {
+  if (e == hipSuccess) return TBG_OK;
+  if (e == hipErrorInvalidConfiguration) return fail(TBG_ERR_UNSUPPORTED, "%s: too many tiles for one launch", what);
+  return fail(TBG_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
+}
+
 }  // namespace
 
 extern "C" {
@@ -256,8 +262,7 @@ tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   } else {
     e = tbg::launch_grouped(p, b, b, ab_dtype == TBG_F16, (int)bl, out_code(c_dtype), s);
   }
-  if (e != hipSuccess) return fail(TBG_ERR_HIP, "grouped gemm launch: %s", hipGetErrorString(e));
-  return TBG_OK;
+  return launch_status("grouped gemm", e);
 }
 
 size_t tbg_gemm_grouped_wgrad_workspace_query(int64_t groups, int64_t M, int64_t P, int64_t Q, tbg_dtype ab_dtype,
@@ -347,8 +352,7 @@ tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t 
                   (ll)groups, (ll)M, (ll)P, (ll)Q, ab_dtype == TBG_F16 ? "f16" : "bf16",
                   c_dtype == TBG_F32 ? "f32" : "16-bit", b, b, rx.needed ? "yes" : "no", ry.needed ? "yes" : "no");
   e = tbg::launch_wgrad(p, b, b, ab_dtype == TBG_F16, out_code(c_dtype), s);
-  if (e != hipSuccess) return fail(TBG_ERR_HIP, "grouped wgrad launch: %s", hipGetErrorString(e));
-  return TBG_OK;
+  return launch_status("grouped wgrad", e);
 }
 
 }  // extern "C"
@@ -482,8 +486,7 @@ tbg_status mx4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, const 
                   few ? "rows" : "ring", few ? 16 : bm, few ? 16 : bn, few ? 1 : stages);
   const hipError_t e = few ? tbg::launch_few_rows(p, 2, out_code(c_dtype), (hipStream_t)stream)
                            : tbg::launch_mx4_gemm(p, bm, bn, stages, c_dtype == TBG_BF16, cus, (hipStream_t)stream);
-  if (e != hipSuccess) return fail(TBG_ERR_HIP, "mx4 gemm launch: %s", hipGetErrorString(e));
-  return TBG_OK;
+  return launch_status("mx4 gemm", e);
 }
 
 }  // namespace

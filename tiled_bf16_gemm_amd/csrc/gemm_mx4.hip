@@ -42,7 +42,7 @@ hipError_t launch_mx4_gemm(Mx4GemmParams p, int bm, int bn, int stages, int out_
     const int64_t walkers = cus >= 8 ? cus / 8 * 8 : 8;
     return launch_mx4_walk<256, 2>(p, out_bf16, (unsigned)(grid < walkers ? grid : walkers), stream);
   }
-  if (grid > kMaxGrid) return hipErrorInvalidValue;
+  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
   const unsigned g = (unsigned)grid;
   if (bm == 128 && bn == 128 && stages == 2) return launch_mx4_tile<128, 128, 2>(p, out_bf16, g, stream);
   if (bm == 64 && bn == 64 && stages == 2) return launch_mx4_tile<64, 64, 2>(p, out_bf16, g, stream);

@@ -23,7 +23,7 @@ hipError_t launch_few_rows(Mx4GemmParams p, int fmt, int out, hipStream_t stream
   if (p.g.offsets) grid = (grid + 7) / 8 * 8;
   else if (p.g.rows > 16) return hipErrorInvalidValue;
   if (grid == 0 || p.g.rows == 0) return hipSuccess;
-  if (grid > kMaxGrid) return hipErrorInvalidValue;
+  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
   if (fmt == kRowsBf16) return launch_rows<kRowsBf16, 1>(p, out, (unsigned)grid, stream);
   if (fmt == kRowsF16) return launch_rows<kRowsF16, 2>(p, out, (unsigned)grid, stream);
   return launch_rows<kRowsMx4, 1>(p, out, (unsigned)grid, stream);

@@ -137,7 +137,8 @@ struct GroupedParams {
 // 256×256, 128×128, 64×64; they fill the tile counts and the grid.
 hipError_t launch_grouped(GroupedParams p, int bm, int bn, int in, int b_layout, int out, hipStream_t stream);
 hipError_t launch_wgrad(GroupedParams p, int bm, int bn, int in, int out, hipStream_t stream);
-// Workgroups one launch takes: it counts its threads (256 a workgroup) in 32 bits.
+// Workgroups one launch takes: it counts its threads (256 a workgroup) in 32 bits.  The launchers of the
+// ragged and the 4-bit products return hipErrorInvalidConfiguration for more.
 constexpr int64_t kMaxGrid = (1 << 24) - 1;
 // Upper bound of the tiles of height bm over any split of `rows` rows into `groups` groups.
 inline int64_t ragged_tiles_bound(int64_t rows, int64_t groups, int64_t bm) {
