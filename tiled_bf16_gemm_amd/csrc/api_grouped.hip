@@ -84,14 +84,33 @@ Repack plan_repack(const void* p, int64_t groups, int64_t stride, int64_t rows, 
   return r;
 }
 
-hipError_t run_repack(const void* src, int64_t groups, int64_t stride, int64_t rows, int64_t cols, int64_t ld,
-                      const Repack& r, uint8_t* dst, hipStream_t s) {
-  tbg::PackJob j{(const uint8_t*)src, ld * 2, rows, cols * 2, dst, r.ld * 2};
-  if (groups == 1 || stride == rows * ld) {
-    j.rows = groups * rows;
-    return tbg::launch_pack_jobs(&j, 1, s);
-  }
-  return tbg::launch_pack_groups(j, groups, stride * 2, s);
+// What a repack reads: as plan_repack.
+struct Operand {
+  const void* p;
+  int64_t groups, stride, rows, cols, ld;
+};
+
+// The repacks of both operands, a's into `area` and b's behind it; a and b then point to the copies.
+// Matrices at one pitch throughout go out in one launch (both operands of a small weight gradient: 15.9 to 13.5 µs
+// a call with the host).
+hipError_t run_repacks(Operand& a, const Repack& ra, Operand& b, const Repack& rb, uint8_t* area, hipStream_t s) {
+  tbg::PackJob jobs[2];
+  int n = 0;
+  hipError_t e = hipSuccess;
+  auto add = [&](Operand& o, const Repack& r, uint8_t* dst) {
+    if (!r.needed) return;
+    tbg::PackJob j{(const uint8_t*)o.p, o.ld * 2, o.rows, o.cols * 2, dst, r.ld * 2};
+    if (o.groups == 1 || o.stride == o.rows * o.ld) {
+      j.rows = o.groups * o.rows;
+      jobs[n++] = j;
+    } else if (e == hipSuccess) {
+      e = tbg::launch_pack_groups(j, o.groups, o.stride * 2, s);
+    }
+    o.p = dst;
+  };
+  add(a, ra, area);
+  add(b, rb, area + ra.bytes);
+  return e == hipSuccess ? tbg::launch_pack_jobs(jobs, n, s) : e;
 }
 
 tbg_status check_workspace(size_t need, const void* workspace, size_t have) {
@@ -221,20 +240,13 @@ tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   const bool few = nk && takes_few_rows(active, (double)M, N, cus);
   hipStream_t s = (hipStream_t)stream;
   uint8_t* const area = tbg::repack_area(workspace, workspace_bytes, ra.bytes + rb.bytes);
-  hipError_t e = hipSuccess;
-  if (ra.needed) {
-    e = run_repack(A, 1, 0, M, K, lda, ra, area, s);
-    A = area;
-  }
-  if (rb.needed && e == hipSuccess) {
-    e = run_repack(B, groups, stride_b, b_rows, b_cols, ldb, rb, area + ra.bytes, s);
-    B = area + ra.bytes;
-  }
+  Operand oa{A, 1, 0, M, K, lda}, ob{B, groups, stride_b, b_rows, b_cols, ldb};
+  hipError_t e = run_repacks(oa, ra, ob, rb, area, s);
   if (e != hipSuccess) return fail(TBG_ERR_HIP, "operand repack: %s", hipGetErrorString(e));
   tbg::GroupedParams p;
   memset(&p, 0, sizeof(p));
-  p.A = (const uint8_t*)A;
-  p.B = (const uint8_t*)B;
+  p.A = (const uint8_t*)oa.p;
+  p.B = (const uint8_t*)ob.p;
   p.C = C;
   p.offsets = offsets;
   p.lda = ra.ld * 2;
@@ -318,20 +330,13 @@ tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t 
   }
   hipStream_t s = (hipStream_t)stream;
   uint8_t* const area = tbg::repack_area(workspace, workspace_bytes, rx.bytes + ry.bytes);
-  hipError_t e = hipSuccess;
-  if (rx.needed) {
-    e = run_repack(X, 1, 0, M, P, ldx, rx, area, s);
-    X = area;
-  }
-  if (ry.needed && e == hipSuccess) {
-    e = run_repack(Y, 1, 0, M, Q, ldy, ry, area + rx.bytes, s);
-    Y = area + rx.bytes;
-  }
+  Operand ox{X, 1, 0, M, P, ldx}, oy{Y, 1, 0, M, Q, ldy};
+  hipError_t e = run_repacks(ox, rx, oy, ry, area, s);
   if (e != hipSuccess) return fail(TBG_ERR_HIP, "operand repack: %s", hipGetErrorString(e));
   tbg::GroupedParams p;
   memset(&p, 0, sizeof(p));
-  p.A = (const uint8_t*)X;
-  p.B = (const uint8_t*)Y;
+  p.A = (const uint8_t*)ox.p;
+  p.B = (const uint8_t*)oy.p;
   p.C = C;
   p.offsets = offsets;
   p.lda = rx.ld * 2;
