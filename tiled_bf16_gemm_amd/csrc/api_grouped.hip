@@ -91,8 +91,8 @@ struct Operand {
 };
 
 // The repacks of both operands, a's into `area` and b's behind it; a and b then point to the copies.
-// Matrices at one pitch throughout go out in one launch (both operands of a small weight gradient: 15.9 to 13.5 µs
-// a call with the host).
+// Matrices at one pitch throughout go out in one launch (both operands of a small weight gradient:
+// 15.9 to 13.5 µs a call with the host).
 hipError_t run_repacks(Operand& a, const Repack& ra, Operand& b, const Repack& rb, uint8_t* area, hipStream_t s) {
   tbg::PackJob jobs[2];
   int n = 0;
