@@ -442,9 +442,11 @@ tbg_status tbg_conv2d_fwd(const tbg_conv2d_shape* shape, float alpha, const void
  *             offsets[e] .. offsets[e+1]-1.  They must not descend and must lie in 0..M; groups
  *             may be empty, and rows before offsets[0] or from offsets[groups] on belong to none.
  *             They are read on `stream` when the work runs, so a captured graph replays with the
- *             offsets then in memory.  Values outside 0..M are taken as the nearer bound and a
- *             descending pair as an empty group: nothing outside the operands is read or written
- *             (but what C then holds in rows that several groups claim is not specified).
+ *             offsets then in memory.  Values outside 0..M are taken as the nearer bound, and
+ *             nothing outside the operands is read or written whatever they are.  The rows'
+ *             products take a value below an earlier one as that one (each row has one group at
+ *             most); the weight gradient takes every pair by itself, a descending one as an empty
+ *             group.
  * Limits: M, N and K (P and Q) up to 2^30, groups up to 4096, leading dimensions of 16-bit
  * operands below 2^22 elements. */
 

@@ -607,3 +607,31 @@ def test_torch_helper_refusals():
                         (A, A, off, dict(out=torch.zeros((2, 16, 15), device="cuda")))):
         with pytest.raises(ValueError):
             ops.gemm_grouped_wgrad(x, y, o, **kw)
+
+
+# Offsets that descend: the pairs together claim more tiles than groups that ascend can make.
+DESCENDING = [
+    (1000, [0, 900, 0, 900, 0, 900, 1000]),
+    (2000, [0, 1900, 0, 2000]),
+    (40, [0, 36, 0, 36, 0, 40]),
+    (3000, [0, 2990] * 100 + [0, 3000]),
+    (700, [100, 600, -7, 90] + [650, 20] * 40 + [1 << 30, 600, 640, 5]),
+]
+
+
+@gpu
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("M,edges", DESCENDING)
+def test_rows_of_descending_offsets_belong_to_the_first_group_that_reaches_them(M, edges, layout):
+    """An offset below an earlier one counts as that one, so every row up to the largest offset has one
+    group, and none is left out."""
+    print(f"rows {layout} descending offsets M={M} groups={len(edges) - 1}", flush=True)
+    gen, dt, G, K = _gen(M), torch.bfloat16, len(edges) - 1, 72
+    good = np.maximum.accumulate(np.clip(edges, 0, M)).tolist()
+    for N in (40, 1032):
+        A, B = _ints(gen, (M, K), dt), _ints(gen, (G, K, N) if layout == "kn" else (G, N, K), dt)
+        out = torch.full((M + 2, N), 7.0, device="cuda")
+        _ops().gemm_grouped(A, B, _dev(edges), layout, "f32", out=out[1:M + 1])
+        want = torch.full((M + 2, N), 7.0, device="cuda")
+        want[1 + good[0]:1 + good[-1]] = _ref_rows(A, B, good, layout)[good[0]:good[-1]].float()
+        assert torch.equal(out, want), N

@@ -553,3 +553,31 @@ def test_torch_helper_refusals():
         ops.mx4_gemm_grouped(c, s, c, s, torch.zeros(2, dtype=torch.int32, device="cuda"))
     with pytest.raises(tbg.Error):
         ops.mx4_gemm(c, s.contiguous(), c, s)  # scale rows two bytes apart
+
+
+@gpu
+@pytest.mark.parametrize("M,edges", [
+    (1000, [0, 900, 0, 900, 0, 900, 1000]),
+    (2000, [0, 1900, 0, 2000]),
+    (40, [0, 36, 0, 36, 0, 40]),
+    (3000, [0, 2990] * 100 + [0, 3000]),
+    (6000, [5, 5900, 0, 5900, 0, 6000]),
+])
+def test_rows_of_descending_offsets_belong_to_the_first_group_that_reaches_them(M, edges):
+    """An offset below an earlier one counts as that one, so every row up to the largest offset has one
+    group, and none is left out (groups that claim more tiles than ascending ones can make)."""
+    print(f"mx4 descending offsets M={M} groups={len(edges) - 1}", flush=True)
+    rng, G, K = np.random.default_rng(M), len(edges) - 1, 96
+    good = np.maximum.accumulate(edges).tolist()
+    a, sa, va = _random_mx4(rng, (M,), K)
+    for N in (40, 3000 if M > 5000 else 500):
+        b, sb, vb = _random_mx4(rng, (G, N), K)
+        out = torch.full((M + 2, N), 7.0, device="cuda")
+        _ops().mx4_gemm_grouped(a, sa, b, sb, torch.tensor(edges, dtype=torch.int32, device="cuda"), "f32",
+                                out=out[1:M + 1])
+        want = torch.full((M + 2, N), 7.0, device="cuda")
+        for e in range(G):
+            lo, hi = good[e], good[e + 1]
+            if lo < hi:
+                want[1 + lo:1 + hi] = (va[lo:hi] @ vb[e].t().contiguous()).float()
+        assert torch.equal(out, want), N

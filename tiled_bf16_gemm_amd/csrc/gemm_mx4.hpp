@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_mx4_walk_kernel(Mx4GemmParam
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RaggedPlan plan{};
-  if (p.g.offsets) plan = ragged_plan<B>(p.g.offsets, p.g.groups, p.g.rows, p.g.tiles_m, p.g.tiles_n);
+  if (p.g.offsets) plan = ragged_plan<B>(p.g.offsets, p.g.groups, p.g.rows, p.g.tiles_n);
   else plan.tiles = p.g.tiles_m * p.g.tiles_n;
   int first, count;
   xcd_share(plan.tiles, blockIdx.x, first, count);

@@ -8,21 +8,23 @@
 // lane counts the tiles of its share of the groups, one prefix sum over the lanes places them, and
 // the lane whose range holds the workgroup's number answers.  That is one dependent load and ≈30
 // vector instructions before the K loop, against a launch of its own (and a table in a workspace)
-// for a planning kernel.  Offsets are clamped to the rows that exist and to ascending pairs, so
-// no value in them takes an access outside the operands; offsets that descend make no more tiles
-// than any others can (tile_rows bounds them: their sum might even pass 32 bits, but the first lane
-// that covers a tile below the bound has not wrapped).
+// for a planning kernel.  Offsets are clamped to the rows that exist and to their running maximum, so
+// no value in them takes an access outside the operands, no row has two groups, and there are never
+// more tiles than the grid was made for.  The maximum over the lanes before costs a dozen dependent
+// instructions and, past 64 groups, a second pass over a lane's offsets: only a wave that
+// meets a descending pair takes it (a ballot in front).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "launch.hpp"
 
 namespace tbg {
 
-// Rows of group g: begin .. end-1, inside 0 .. rows whatever the offsets hold.
-__device__ __forceinline__ void group_rows(const int32_t* offsets, int g, int rows, int& begin, int& end) {
-  begin = min(max(offsets[g], 0), rows);
+// Rows of group g: begin .. end-1, inside least .. rows whatever the offsets hold (0 <= least <= rows).
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int g, int least, int rows, int& begin, int& end) {
+  begin = min(max(offsets[g], least), rows);
   end = min(max(offsets[g + 1], begin), rows);
 }
 
@@ -36,6 +38,20 @@ __device__ __forceinline__ int wave_prefix_sum(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
   return v;
+}
+
+// Maximum over the lanes before this one (lane 0: 0) of a value that is not negative; all lanes
+// active.
+__device__ __forceinline__ int wave_max_before(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // as wave_prefix_sum
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
+  const int lane = threadIdx.x & 63;
+  const int before = __builtin_amdgcn_ds_bpermute(4 * (lane - 1), v);
+  return lane > 0 ? before : 0;
 }
 
 // Tile `id` of a group's tiles_m × tiles_n: column-major inside bands of tile rows, so that the
@@ -62,24 +78,35 @@ struct RaggedTile {
 // Tiles of BM rows over the groups, and each lane's share of them.
 struct RaggedPlan {
   int upto, mine;  // tile rows up to and with this lane's groups; in them
+  int least;       // no row below this belongs to this lane's groups (0 where no offsets descend)
   int begin, end;  // the rows of this lane's group (up to 64 groups)
   int tiles;       // tiles of all groups
 };
 
 template <int BM>
-__device__ __forceinline__ RaggedPlan ragged_plan(const int32_t* offsets, int groups, int rows, int tile_rows,
-                                                  int tiles_n) {
+__device__ __forceinline__ RaggedPlan ragged_plan(const int32_t* offsets, int groups, int rows, int tiles_n) {
   const int per = (groups + 63) >> 6, g0 = (threadIdx.x & 63) * per;
   RaggedPlan p;
-  p.mine = p.begin = p.end = 0;
-  for (int j = 0; j < per; ++j) {
-    if (g0 + j < groups) {
-      group_rows(offsets, g0 + j, rows, p.begin, p.end);
-      p.mine += (p.end - p.begin + BM - 1) / BM;
+  p.least = 0;
+  bool descends = false;
+  auto count = [&](auto first) __attribute__((always_inline)) {
+    p.mine = p.begin = 0;
+    p.end = p.least;
+    for (int j = 0; j < per; ++j) {
+      if (g0 + j < groups) {
+        if (decltype(first)::value) descends |= offsets[g0 + j + 1] < offsets[g0 + j];
+        group_rows(offsets, g0 + j, p.end, rows, p.begin, p.end);
+        p.mine += (p.end - p.begin + BM - 1) / BM;
+      }
     }
+  };
+  count(std::true_type{});
+  if (__ballot(descends) != 0) {
+    p.least = wave_max_before(p.end);
+    count(std::false_type{});
   }
   p.upto = wave_prefix_sum(p.mine);
-  p.tiles = min(__builtin_amdgcn_readlane(p.upto, 63) * tiles_n, tile_rows * tiles_n);
+  p.tiles = __builtin_amdgcn_readlane(p.upto, 63) * tiles_n;
   return p;
 }
 
@@ -90,10 +117,10 @@ __device__ __forceinline__ void ragged_find(const RaggedPlan& p, const int32_t* 
                                             int tiles_n, int height, int lid, RaggedTile& t) {
   const int per = (groups + 63) >> 6, g0 = (threadIdx.x & 63) * per;
   int at = (p.upto - p.mine) * tiles_n;  // this lane's first tile
-  int found = -1, fb = 0, fe = 0, fi = 0, begin = p.begin, end = p.end;
+  int found = -1, fb = 0, fe = 0, fi = 0, begin = p.begin, end = per > 1 ? p.least : p.end;
   for (int j = 0; j < per; ++j) {
     if (g0 + j < groups) {
-      if (per > 1) group_rows(offsets, g0 + j, rows, begin, end);
+      if (per > 1) group_rows(offsets, g0 + j, end, rows, begin, end);
       const int n = (end - begin + BM - 1) / BM * tiles_n;
       if (lid >= at && lid < at + n) {
         found = g0 + j;
@@ -124,7 +151,7 @@ __device__ __forceinline__ void xcd_share(int tiles, int bid, int& first, int& c
 // The tile of workgroup `bid`, one tile each; false when there is none (the grid is an upper bound).
 template <int BM>
 __device__ __forceinline__ bool ragged_tile(const GroupedParams& g, int height, int bid, RaggedTile& t) {
-  const RaggedPlan p = ragged_plan<BM>(g.offsets, g.groups, g.rows, g.tiles_m, g.tiles_n);
+  const RaggedPlan p = ragged_plan<BM>(g.offsets, g.groups, g.rows, g.tiles_n);
   int first, count;
   xcd_share(p.tiles, bid, first, count);
   if ((bid >> 3) >= count) return false;
@@ -155,7 +182,7 @@ __device__ __forceinline__ bool grad_tile(const GroupedParams& p, int bid, GradT
   int g = place, begin, end;
   if (p.by_rows) {
     int b = 0, e = 0;
-    if (lane < p.groups) group_rows(p.offsets, lane, p.rows, b, e);
+    if (lane < p.groups) group_rows(p.offsets, lane, 0, p.rows, b, e);
     const int rows = lane < p.groups ? e - b : -1;
     int rank = 0;  // groups that run before this lane's: more rows, or as many and an earlier number
     for (int j = 0; j < p.groups; ++j) {
@@ -166,7 +193,7 @@ __device__ __forceinline__ bool grad_tile(const GroupedParams& p, int bid, GradT
     begin = __builtin_amdgcn_readlane(b, g);
     end = __builtin_amdgcn_readlane(e, g);
   } else {
-    group_rows(p.offsets, g, p.rows, begin, end);
+    group_rows(p.offsets, g, 0, p.rows, begin, end);
     begin = __builtin_amdgcn_readfirstlane(begin);
     end = __builtin_amdgcn_readfirstlane(end);
   }
