@@ -635,3 +635,29 @@ def test_rows_of_descending_offsets_belong_to_the_first_group_that_reaches_them(
         want = torch.full((M + 2, N), 7.0, device="cuda")
         want[1 + good[0]:1 + good[-1]] = _ref_rows(A, B, good, layout)[good[0]:good[-1]].float()
         assert torch.equal(out, want), N
+
+
+@gpu
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_one_row_at_any_pitch(layout):
+    """The last token of one sequence: a single row whose stride in the hidden states, never used, passes
+    the largest leading dimension; matrices of a single row likewise, and the weight gradient."""
+    gen, dt, K, N = _gen(77), torch.bfloat16, 4096, 40
+    hidden = _ints(gen, (1, 1100, K), dt)
+    A = hidden[:, -1]
+    assert A.stride(0) >= 1 << 22
+    B = _ints(gen, (1, N, K) if layout == "nk" else (1, K, N), dt)
+    out = _ops().gemm_grouped(A, B, _dev([0, 1]), layout, "f32")
+    assert torch.equal(out.double(), _ref_rows(A, B, [0, 1], layout))
+    grad = _ops().gemm_grouped_wgrad(A, out.to(dt), _dev([0, 1]))
+    assert torch.equal(grad.double(), _ref_wgrad(A, out.to(dt), [0, 1]))
+    wide = torch.full((2, 1, 1 << 23), float("nan"), dtype=dt, device="cuda")
+    X = _ints(gen, (9, 24), dt)
+    one = wide[:, :, :24] if layout == "nk" else wide[:, :, :16]
+    one.copy_(_ints(gen, one.shape, dt))
+    X = X if layout == "nk" else X[:, :1]
+    got = _ops().gemm_grouped(X, one, _dev([0, 4, 9]), layout, "f32")
+    assert torch.equal(got.double(), _ref_rows(X, one, [0, 4, 9], layout))
+    C = torch.full((1, 1, 1 << 23), 5.0, device="cuda")[:, 0, :N]
+    _ops().gemm_grouped(A, B, _dev([0, 1]), layout, "f32", out=C)
+    assert torch.equal(C, out)

@@ -151,9 +151,10 @@ def _require_rows(t: torch.Tensor, name: str, index: int, dims: int = 2):
 
 
 def _pitch(shape, strides) -> int:
-    """Row stride of a matrix, or of each matrix of a stack: a single row's is never used, whatever
-    torch says it is."""
-    return strides[-2] if shape[-2] > 1 else max(strides[-2], shape[-1], 1)
+    """Row stride of a matrix, or of each matrix of a stack.  A single row's is never used, and torch may
+    call it anything (a token of a long sequence: past the largest leading dimension): its length, rounded
+    up to 8 values, stands in for it."""
+    return strides[-2] if shape[-2] > 1 else max(-(-shape[-1] // 8) * 8, 1)
 
 
 def _output(out: Optional[torch.Tensor], shape, out_dtype: str, allowed, index: int) -> torch.Tensor:
