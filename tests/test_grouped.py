@@ -661,3 +661,16 @@ def test_one_row_at_any_pitch(layout):
     C = torch.full((1, 1, 1 << 23), 5.0, device="cuda")[:, 0, :N]
     _ops().gemm_grouped(A, B, _dev([0, 1]), layout, "f32", out=C)
     assert torch.equal(C, out)
+
+
+@gpu
+def test_a_sum_with_c_needs_c():
+    """beta·C without the matrix that holds C would add what new memory happens to hold."""
+    ops, dt = _ops(), torch.bfloat16
+    A, B, off = torch.ones((8, 32), dtype=dt, device="cuda"), torch.ones((2, 24, 32), dtype=dt, device="cuda"), _dev([0, 3, 8])
+    (a, sa), (b, sb) = ops.mx4_quantize(A), ops.mx4_quantize(B)
+    for call in (lambda **k: ops.gemm_grouped(A, B, off, "nk", **k), lambda **k: ops.gemm_grouped_wgrad(A, A, off, **k),
+                 lambda **k: ops.mx4_gemm(a, sa, b[0], sb[0], **k), lambda **k: ops.mx4_gemm_grouped(a, sa, b, sb, off, **k)):
+        with pytest.raises(ValueError, match="beta"):
+            call(beta=1.0)
+        assert call(beta=0.0).isfinite().all()

@@ -157,12 +157,14 @@ def _pitch(shape, strides) -> int:
     return strides[-2] if shape[-2] > 1 else max(-(-shape[-1] // 8) * 8, 1)
 
 
-def _output(out: Optional[torch.Tensor], shape, out_dtype: str, allowed, index: int) -> torch.Tensor:
-    """The caller's `out`, checked, or a new tensor."""
+def _output(out: Optional[torch.Tensor], shape, out_dtype: str, allowed, index: int, beta: float = 0.0) -> torch.Tensor:
+    """The caller's `out`, checked, or a new tensor (which holds no C that beta could scale)."""
     if out_dtype not in allowed:
         raise ValueError(f"out_dtype must be one of {', '.join(allowed)} (got {out_dtype!r})")
     dtype = _TORCH_OF[out_dtype]
     if out is None:
+        if beta != 0.0:
+            raise ValueError(f"beta={beta} needs out, which holds the old C")
         return torch.empty(shape, dtype=dtype, device=index)
     if out.dtype != dtype or tuple(out.shape) != shape or out.get_device() != index:
         raise ValueError(f"out must be a {shape} {dtype} tensor on cuda:{index} (got {tuple(out.shape)} {out.dtype} on "
@@ -192,7 +194,7 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, b_layo
     """C[r] = alpha·A[r]·B[e] + beta·C[r] for the rows r of every group e (offsets[e] <= r <
     offsets[e+1]) through tbg_gemm_grouped.  A: (M, K) bf16 or fp16; B: (groups, K, N) for "kn" or
     (groups, N, K) for "nk"; offsets: (groups + 1,) int32 on the device.  out_dtype: "f32" or A's
-    type.  Rows of no group keep what `out` holds (without `out`: undefined).
+    type.  Rows of no group keep what `out` holds (without `out`: undefined); beta != 0 needs `out`.
     Gradients, for dC of C's shape: of the rows gemm_grouped(dC, B, offsets, the other layout), of B
     gemm_grouped_wgrad(A, dC, offsets) for "kn" and gemm_grouped_wgrad(dC, A, offsets) for "nk"."""
     index = A.get_device()
@@ -213,7 +215,7 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, b_layo
     if matrices != groups:
         raise ValueError(f"B holds {matrices} matrices, offsets {groups} groups")
     with _Launch(index, stream) as handle:
-        out = _output(out, (M, N), out_dtype, ("f32", ab), index)
+        out = _output(out, (M, N), out_dtype, ("f32", ab), index, beta)
         a, b = A.data_ptr(), B.data_ptr()
         lda, ldb, sb = _pitch((M, K), st_a), _pitch(shape_b, st_b), st_b[0]
         # whole 16-byte rows everywhere need no repack; the query knows the exact rule
@@ -230,8 +232,8 @@ def gemm_grouped_wgrad(X: torch.Tensor, Y: torch.Tensor, offsets: torch.Tensor, 
                        stream: Optional[torch.cuda.Stream] = None, alpha: float = 1.0,
                        beta: float = 0.0) -> torch.Tensor:
     """C[e] = alpha·X[rows of e]ᵀ·Y[rows of e] + beta·C[e] through tbg_gemm_grouped_wgrad.  X: (M, P),
-    Y: (M, Q), bf16 or fp16; out: (groups, P, Q) of type "f32" or X's.  An empty group's C is
-    beta·C (zeros when beta == 0)."""
+    Y: (M, Q), bf16 or fp16; out: (groups, P, Q) of type "f32" or X's, needed when beta != 0.  An empty
+    group's C is beta·C (zeros when beta == 0)."""
     index = X.get_device()
     (M, P), st_x = _require_rows(X, "X", index)
     (My, Q), st_y = _require_rows(Y, "Y", index)
@@ -242,7 +244,7 @@ def gemm_grouped_wgrad(X: torch.Tensor, Y: torch.Tensor, offsets: torch.Tensor, 
     if My != M:
         raise ValueError(f"X has {M} rows, Y {My}")
     with _Launch(index, stream) as handle:
-        out = _output(out, (groups, P, Q), out_dtype, ("f32", ab), index)
+        out = _output(out, (groups, P, Q), out_dtype, ("f32", ab), index, beta)
         x, y, st_c = X.data_ptr(), Y.data_ptr(), out.stride()
         ldx, ldy = _pitch((M, P), st_x), _pitch((M, Q), st_y)
         need = 0 if (ldx | ldy) % 8 == 0 and (x | y) % 16 == 0 else \
@@ -356,14 +358,14 @@ def mx4_gemm(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_scales:
              beta: float = 0.0) -> torch.Tensor:
     """C = alpha·A·Bᵀ + beta·C for microscaled 4-bit A (M, K/2 codes) and B (N, K/2 codes), each with
     its scales (rows, K/32), through tbg_mx4_gemm.  Codes and scales 16-byte aligned and pitched, as
-    mx4_quantize makes them."""
+    mx4_quantize makes them; beta != 0 needs `out`."""
     index = A.get_device()
     (M, half), lda, ld_as = _require_mx4(A, a_scales, "A", index, (2,))
     (N, half_b), ldb, ld_bs = _require_mx4(B, b_scales, "B", index, (2,))
     if half != half_b:
         raise ValueError(f"inner sizes differ: {2 * half} vs {2 * half_b}")
     with _Launch(index, stream) as handle:
-        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), index)
+        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), index, beta)
         tbg.mx4_gemm(M, N, 2 * half, alpha, A.data_ptr(), lda, a_scales.data_ptr(), ld_as, B.data_ptr(), ldb,
                      b_scales.data_ptr(), ld_bs, beta, out.data_ptr(), _pitch((M, N), out.stride()), out_dtype, handle)
     return out
@@ -374,7 +376,7 @@ def mx4_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b
                      stream: Optional[torch.cuda.Stream] = None, alpha: float = 1.0, beta: float = 0.0) -> torch.Tensor:
     """mx4_gemm for the rows of every group (offsets as gemm_grouped) with its own B, (groups, N, K/2
     codes), through tbg_mx4_gemm_grouped.  Rows of no group keep what `out` holds (without `out`:
-    undefined)."""
+    undefined); beta != 0 needs `out`."""
     index = A.get_device()
     (M, half), lda, ld_as = _require_mx4(A, a_scales, "A", index, (2,))
     (matrices, N, half_b), ldb, ld_bs = _require_mx4(B, b_scales, "B", index, (3,))
@@ -384,7 +386,7 @@ def mx4_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b
     if matrices != groups:
         raise ValueError(f"B holds {matrices} matrices, offsets {groups} groups")
     with _Launch(index, stream) as handle:
-        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), index)
+        out = _output(out, (M, N), out_dtype, ("f32", "bf16"), index, beta)
         tbg.mx4_gemm_grouped(groups, M, N, 2 * half, offsets.data_ptr(), alpha, A.data_ptr(), lda, a_scales.data_ptr(),
                              ld_as, B.data_ptr(), ldb, B.stride(0), b_scales.data_ptr(), ld_bs, b_scales.stride(0),
                              beta, out.data_ptr(), _pitch((M, N), out.stride()), out_dtype, handle)
