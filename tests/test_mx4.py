@@ -581,3 +581,17 @@ def test_rows_of_descending_offsets_belong_to_the_first_group_that_reaches_them(
             if lo < hi:
                 want[1 + lo:1 + hi] = (va[lo:hi] @ vb[e].t().contiguous()).float()
         assert torch.equal(out, want), N
+
+
+@gpu
+def test_rows_without_a_column():
+    """K == 0 from end to end: no codes, no scales, and the empty sum."""
+    ops = _ops()
+    x, w = torch.zeros((5, 0), device="cuda"), torch.zeros((2, 7, 0), device="cuda")
+    (a, sa), (b, sb) = ops.mx4_quantize(x), ops.mx4_quantize(w)
+    assert ops.mx4_dequantize(a, sa, cols=0).shape == (5, 0)
+    out = ops.mx4_gemm(a, sa, b[0], sb[0], "f32", out=torch.full((5, 7), float("nan"), device="cuda"))
+    assert (out == 0).all()
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    out = ops.mx4_gemm_grouped(a, sa, b, sb, off, "f32", out=torch.full((5, 7), 3.0, device="cuda"), beta=2.0)
+    assert (out[:4] == 6).all() and (out[4] == 3).all()

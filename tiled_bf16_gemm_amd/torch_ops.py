@@ -257,7 +257,7 @@ def gemm_grouped_wgrad(X: torch.Tensor, Y: torch.Tensor, offsets: torch.Tensor, 
 
 def _require_mx4(codes: torch.Tensor, scales: torch.Tensor, name: str, index: int, dims=(2, 3)):
     """Codes and scales that belong together, on device `index`: the codes' shape and both pitches in
-    bytes (a single row's pitch is its length rounded up to 16)."""
+    bytes (a single row's pitch is its length rounded up to 16, that of rows without a value 0)."""
     shape, blocks, st, st_s = codes.shape, scales.shape, codes.stride(), scales.stride()
     if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise ValueError(f"{name}'s codes and scales must be uint8 tensors")
@@ -274,7 +274,7 @@ def _require_mx4(codes: torch.Tensor, scales: torch.Tensor, name: str, index: in
                          "codes and one scale per 32 values)")
     if (st[-1] != 1 and half > 1) or (st_s[-1] != 1 and nb > 1):
         raise ValueError(f"{name}'s codes and scales must have a unit inner stride")
-    if rows > 1:
+    if rows > 1 and half > 0:
         return shape, st[-2], st_s[-2]
     return shape, half, -(-nb // 16) * 16
 
