@@ -448,7 +448,9 @@ tbg_status tbg_conv2d_fwd(const tbg_conv2d_shape* shape, float alpha, const void
  *             most); the weight gradient takes every pair by itself, a descending one as an empty
  *             group.
  * Limits: M, N and K (P and Q) up to 2^30, groups up to 4096, leading dimensions of 16-bit
- * operands below 2^22 elements. */
+ * operands below 2^22 elements, and fewer than 2^24 workgroups (output tiles of 256, 128 or 64 rows
+ * and columns, 64 where a group has up to 64 rows; one row: N up to 2^30 - 512).  A call past a limit
+ * is refused before anything is enqueued. */
 
 /* Workspace bytes tbg_gemm_grouped needs for these operands (only compared against 16-byte
  * boundaries, never dereferenced): A is repacked when lda % 8, K % 8 or A % 16 is non-zero; B
@@ -527,8 +529,9 @@ tbg_status tbg_mx4_dequantize(int64_t rows, int64_t cols, const void* codes, int
 /* C <- alpha·A·Bᵀ + beta·C for 4-bit A (M×K) and B (stored N×K) on the scaled matrix instruction,
  * fp32 accumulation, C TBG_F32 or TBG_BF16 (row-major, ldc >= N).  alpha, beta as tbg_gemm_ex.  K is
  * a multiple of 32 (columns that quantisation added are zeros and change nothing).
- * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.  Limits: sizes up to 2^30, pitches of codes
- * below 2^23 bytes.
+ * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.  Limits: sizes up to 2^30, pitches of codes and
+ * scales below 2^23 bytes, workgroups as for the ragged products (the largest tiles have no such
+ * limit).
  * Returns INVALID_VALUE (negative sizes, K % 32, pitches too small, null pointers, C type),
  * MISALIGNED (codes, scales or pitches off 16), UNSUPPORTED (limits), NO_DEVICE / HIP. */
 tbg_status tbg_mx4_gemm(int64_t M, int64_t N, int64_t K, float alpha, const void* A, int64_t lda, const void* A_scales,

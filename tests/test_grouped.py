@@ -674,3 +674,20 @@ def test_a_sum_with_c_needs_c():
         with pytest.raises(ValueError, match="beta"):
             call(beta=1.0)
         assert call(beta=0.0).isfinite().all()
+
+
+@gpu
+def test_a_refused_call_enqueues_nothing():
+    """2^24 workgroups of 64 columns over rows that need a repack (K = 1): refused as unsupported, and the
+    workspace is as it was."""
+    N = 1 << 30
+    A, B = torch.ones((1, 1), dtype=torch.bfloat16, device="cuda"), torch.ones((1, N, 1), dtype=torch.bfloat16, device="cuda")
+    C = torch.empty((1, N), dtype=torch.bfloat16, device="cuda")
+    need = tbg.gemm_grouped_workspace_query(1, 1, N, 1, "bf16", A.data_ptr(), 1, B.data_ptr(), 1, N, "nk")
+    assert need > 16 * N
+    ws = torch.full((need // 8,), 0x5A5A5A5A, dtype=torch.int64, device="cuda")
+    with pytest.raises(tbg.Error) as e:
+        _ops().gemm_grouped(A, B, _dev([0, 1]), "nk", "bf16", out=C, workspace=ws)
+    assert e.value.status == tbg.ERR_UNSUPPORTED, e.value
+    torch.cuda.synchronize()
+    assert all((part == 0x5A5A5A5A).all() for part in ws.split(1 << 26))

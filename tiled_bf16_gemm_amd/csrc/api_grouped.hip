@@ -1,13 +1,13 @@
 // The C ABI of the ragged and the 4-bit products (include/tbg.h): argument checks, repacking and the
 // choice of a tile.  Host code only; kernels are enqueued on the caller's stream.
 #include <hip/hip_runtime.h>
-#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
 #include "api_util.hpp"
 #include "launch.hpp"
 #include "tbg.h"
+#include "tile_choice.hpp"
 
 using tbg::check_device;
 using tbg::fail;
@@ -121,66 +121,16 @@ tbg_status check_workspace(size_t need, const void* workspace, size_t have) {
   return TBG_OK;
 }
 
-// ---- the choice of a tile -------------------------------------------------------------------
-// A round of tiles, one on every slot the chip has for them, takes about `fixed` µs to start and to
-// store and `per` µs for each K tile (128 bytes of a row); the smaller tiles share a CU, and a
-// round that does not fill costs them only `part` of one, since the next tiles start as others end.
-// The figures are fitted to every tile's time on thousands of shapes (MI355X, 4 to 64 groups of 70 to
-// 2048 rows on average, N of 256 to 14336, K of 256 to 8192; the 4-bit ones also dense): the tile
-// chosen takes 1.0 % (16-bit rows), 1.4 % (weight gradient) and 0.9 % (4 bits) longer than the
-// best one on average.
-struct TileTime {
-  int b, per_cu;
-  double fixed, per, part;
-};
-const TileTime kTilesRows[] = {{256, 1, 9.2, 0.98, 1.0}, {128, 2, 3.65, 0.97, 0.13}, {64, 3, 2.3, 0.61, 0.58}};
-const TileTime kTilesGrad[] = {{256, 1, 14.2, 0.88, 1.0}, {128, 2, 4.1, 1.05, 0.1}, {64, 3, 4.6, 0.52, 0.45}};
-const TileTime kTiles4[] = {{256, 1, 10.5, 0.98, 1.0}, {128, 2, 4.1, 1.05, 0.135}, {64, 2, 4.2, 0.42, 0.63}};
-
-double tile_time(const TileTime& t, double tiles, double ktiles, int cus) {
-  double rounds = tiles / ((double)t.per_cu * cus);
-  if (rounds <= 1) rounds = 1;
-  else if (t.part == 1.0) rounds = ceil(rounds);
-  else rounds += t.part;
-  return rounds * (t.fixed + t.per * ktiles);
-}
-
-// The tile for `groups` groups that share `rows` rows.  How the rows split is not known here:
-// groups of the average size are assumed, each ending half way into its last tile.  Up to 64 (128)
-// rows a group the product is bound by the bytes of B, which a tile of 64 (128) rows reads as
-// well with less of it masked (64 groups, N = K = 2048, 16 bits: 64 rows 130 µs with 64-row tiles,
-// 153 with 128; 128 rows 159 µs with 128, 182 with 256).
-int choose_rows_tile(const TileTime (&t)[3], double groups, double rows, int64_t N, double ktiles, int cus) {
-  const double average = rows / groups;
-  int best = 64;
-  double best_time = 0;
-  for (const TileTime& c : t) {
-    if ((c.b > 64 && average <= 64) || (c.b > 128 && average <= 128)) continue;
-    const double per = groups > 1 ? average / c.b + 0.5 : ceil(average / c.b);
-    const double tiles = groups * (per > 1 ? per : 1) * (double)((N + c.b - 1) / c.b);
-    const double time = tile_time(c, tiles, ktiles, cus);
-    if (best_time == 0 || time < best_time) {
-      best = c.b;
-      best_time = time;
-    }
-  }
-  return best;
-}
-
-// Tiles of 64 columns that groups of up to 64 rows make.
-double narrow_tiles(double groups, int64_t N) { return groups * (double)((N + 63) / 64); }
-
-// Whether the kernel of few rows (gemm_rows.hpp, with both sides' figures) takes a product.
-bool takes_few_rows(double groups, double rows, int64_t N, int cus) {
-  return rows <= 16 * groups && narrow_tiles(groups, N) < 0.75 * cus;
-}
-
-bool too_many_tiles(int64_t tiles) { return tiles > INT32_MAX - 8; }
-
 tbg_status launch_status(const char* what, hipError_t e) {
   if (e == hipSuccess) return TBG_OK;
-  if (e == hipErrorInvalidConfiguration) return fail(TBG_ERR_UNSUPPORTED, "%s: too many tiles for one launch", what);
   return fail(TBG_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+// More workgroups than one launch takes: refused before anything is enqueued.
+tbg_status check_grid(const tbg::TileChoice& c) {
+  if (c.fits()) return TBG_OK;
+  return fail(TBG_ERR_UNSUPPORTED, "too many tiles for one launch (%lld x %lld of %dx%d)", (ll)c.tiles_m, (ll)c.tiles_n,
+              c.bm, c.bn);
 }
 
 }  // namespace
@@ -230,14 +180,12 @@ tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   const Repack rb = plan_repack(B, groups, stride_b, b_rows, b_cols, ldb, nk);
   st = check_workspace(ra.bytes + rb.bytes, workspace, workspace_bytes);
   if (st != TBG_OK) return st;
-  if (too_many_tiles(tbg::ragged_tiles_bound(M, groups, 16) * ((N + 15) / 16)))
-    return fail(TBG_ERR_UNSUPPORTED, "too many tiles for one launch (M=%lld, N=%lld)", (ll)M, (ll)N);
   int cus = 0;
   st = check_device(&cus);
   if (st != TBG_OK) return st;
-  const double active = (double)(groups < M ? groups : M);
-  const int b = choose_rows_tile(kTilesRows, active, (double)M, N, ceil(K / 64.0), cus);
-  const bool few = nk && takes_few_rows(active, (double)M, N, cus);
+  const tbg::TileChoice choice = tbg::choose_grouped(groups, M, N, K, nk, cus);
+  st = check_grid(choice);
+  if (st != TBG_OK) return st;
   hipStream_t s = (hipStream_t)stream;
   uint8_t* const area = tbg::repack_area(workspace, workspace_bytes, ra.bytes + rb.bytes);
   Operand oa{A, 1, 0, M, K, lda}, ob{B, groups, stride_b, b_rows, b_cols, ldb};
@@ -264,15 +212,15 @@ tbg_status tbg_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, con
   p.scaled = scaled ? 1 : 0;
   tbg::log_choice("grouped gemm groups=%lld M=%lld N=%lld K=%lld B=%s in=%s out=%s: %s %dx%d; repack A %s, B %s",
                   (ll)groups, (ll)M, (ll)N, (ll)K, nk ? "nk" : "kn", ab_dtype == TBG_F16 ? "f16" : "bf16",
-                  c_dtype == TBG_F32 ? "f32" : "16-bit", few ? "rows" : "ring", few ? 16 : b, few ? 16 : b,
+                  c_dtype == TBG_F32 ? "f32" : "16-bit", choice.few ? "rows" : "ring", choice.bm, choice.bn,
                   ra.needed ? "yes" : "no", rb.needed ? "yes" : "no");
-  if (few) {
+  if (choice.few) {
     tbg::Mx4GemmParams q;
     memset(&q, 0, sizeof(q));
     q.g = p;
-    e = tbg::launch_few_rows(q, ab_dtype == TBG_F16, out_code(c_dtype), s);
+    e = tbg::launch_few_rows(q, choice, ab_dtype == TBG_F16, out_code(c_dtype), s);
   } else {
-    e = tbg::launch_grouped(p, b, b, ab_dtype == TBG_F16, (int)bl, out_code(c_dtype), s);
+    e = tbg::launch_grouped(p, choice, ab_dtype == TBG_F16, (int)bl, out_code(c_dtype), s);
   }
   return launch_status("grouped gemm", e);
 }
@@ -312,22 +260,12 @@ tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t 
   const Repack rx = plan_repack(X, 1, 0, M, P, ldx, false), ry = plan_repack(Y, 1, 0, M, Q, ldy, false);
   st = check_workspace(rx.bytes + ry.bytes, workspace, workspace_bytes);
   if (st != TBG_OK) return st;
-  if (too_many_tiles(groups * ((P + 63) / 64) * ((Q + 63) / 64)))
-    return fail(TBG_ERR_UNSUPPORTED, "too many tiles for one launch (P=%lld, Q=%lld)", (ll)P, (ll)Q);
   int cus = 0;
   st = check_device(&cus);
   if (st != TBG_OK) return st;
-  // Every group has the same tiles, its rows are the sum's terms.
-  int b = 0;
-  double best = 0;
-  for (const TileTime& t : kTilesGrad) {
-    const double tiles = (double)groups * (double)((P + t.b - 1) / t.b) * (double)((Q + t.b - 1) / t.b);
-    const double time = tile_time(t, tiles, ceil((double)M / (double)groups / 64), cus);
-    if (!b || time < best) {
-      b = t.b;
-      best = time;
-    }
-  }
+  const tbg::TileChoice choice = tbg::choose_wgrad(groups, M, P, Q, cus);
+  st = check_grid(choice);
+  if (st != TBG_OK) return st;
   hipStream_t s = (hipStream_t)stream;
   uint8_t* const area = tbg::repack_area(workspace, workspace_bytes, rx.bytes + ry.bytes);
   Operand ox{X, 1, 0, M, P, ldx}, oy{Y, 1, 0, M, Q, ldy};
@@ -355,8 +293,8 @@ tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t 
   p.scaled = scaled ? 1 : 0;
   tbg::log_choice("grouped wgrad groups=%lld M=%lld P=%lld Q=%lld in=%s out=%s: ring %dx%d; repack X %s, Y %s",
                   (ll)groups, (ll)M, (ll)P, (ll)Q, ab_dtype == TBG_F16 ? "f16" : "bf16",
-                  c_dtype == TBG_F32 ? "f32" : "16-bit", b, b, rx.needed ? "yes" : "no", ry.needed ? "yes" : "no");
-  e = tbg::launch_wgrad(p, b, b, ab_dtype == TBG_F16, out_code(c_dtype), s);
+                  c_dtype == TBG_F32 ? "f32" : "16-bit", choice.bm, choice.bn, rx.needed ? "yes" : "no", ry.needed ? "yes" : "no");
+  e = tbg::launch_wgrad(p, choice, ab_dtype == TBG_F16, out_code(c_dtype), s);
   return launch_status("grouped wgrad", e);
 }
 
@@ -442,26 +380,12 @@ tbg_status mx4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, const 
   }
   if (groups == 0 || M == 0 || N == 0) return TBG_OK;
   if (!C) return fail(TBG_ERR_INVALID_VALUE, "C is NULL");
-  const int64_t worst = (ragged ? tbg::ragged_tiles_bound(M, groups, 64) : (M + 15) / 16) * ((N + 15) / 16);
-  if (too_many_tiles(worst)) return fail(TBG_ERR_UNSUPPORTED, "too many tiles for one launch (M=%lld, N=%lld)", (ll)M, (ll)N);
   int cus = 0;
   st = check_device(&cus);
   if (st != TBG_OK) return st;
-  const double active = ragged ? (double)(groups < M ? groups : M) : 1.0;
-  const bool few = takes_few_rows(active, (double)M, N, cus) && (ragged || M <= 16);
-  // Up to 32 rows a group: 32-row tiles, which copy half as many masked rows of A as 64-row ones (40
-  // groups of one or two rows, N = 4096, K = 2048: 34.7 against 40.0 µs).  Two stages instead of four
-  // let more workgroups share a CU, which pays once there are enough of them (the same product
-  // 34.7 against 40.4 µs); few workgroups need the depth (N = 8192, K = 8192, one row: 17.6 against
-  // 10.0 µs).
-  int bm = 0, bn = 0, stages = 2;
-  if ((double)M <= 32 * active) {
-    bm = 32;
-    bn = 64;
-  } else {
-    bm = bn = choose_rows_tile(kTiles4, active, (double)M, N, ceil(K / 256.0), cus);
-  }
-  if (bn == 64 && narrow_tiles(active, N) * ((double)M / active > bm ? (double)M / active / bm : 1) < 4 * cus) stages = 4;
+  const tbg::TileChoice choice = tbg::choose_mx4(ragged ? groups : 0, M, N, K, cus);
+  st = check_grid(choice);
+  if (st != TBG_OK) return st;
   tbg::Mx4GemmParams p;
   memset(&p, 0, sizeof(p));
   p.g.A = (const uint8_t*)A;
@@ -488,9 +412,9 @@ tbg_status mx4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, const 
   p.stride_bs = stride_bs;
   tbg::log_choice("mx4 gemm groups=%lld M=%lld N=%lld K=%lld out=%s: %s %dx%d, %d stages",
                   (ll)(ragged ? groups : 1), (ll)M, (ll)N, (ll)K, c_dtype == TBG_F32 ? "f32" : "bf16",
-                  few ? "rows" : "ring", few ? 16 : bm, few ? 16 : bn, few ? 1 : stages);
-  const hipError_t e = few ? tbg::launch_few_rows(p, 2, out_code(c_dtype), (hipStream_t)stream)
-                           : tbg::launch_mx4_gemm(p, bm, bn, stages, c_dtype == TBG_BF16, cus, (hipStream_t)stream);
+                  choice.few ? "rows" : "ring", choice.bm, choice.bn, choice.stages);
+  const hipError_t e = choice.few ? tbg::launch_few_rows(p, choice, 2, out_code(c_dtype), (hipStream_t)stream)
+                                  : tbg::launch_mx4_gemm(p, choice, c_dtype == TBG_BF16, (hipStream_t)stream);
   return launch_status("mx4 gemm", e);
 }
 

@@ -12,31 +12,25 @@ hipError_t launch_grouped_tile(const GroupedParams& p, int in, int b_layout, int
 template <int B, int S>
 hipError_t launch_wgrad_tile(const GroupedParams& p, int in, int out, unsigned grid, hipStream_t stream);
 
-hipError_t launch_grouped(GroupedParams p, int bm, int bn, int in, int b_layout, int out, hipStream_t stream) {
-  p.tiles_n = (p.N + bn - 1) / bn;
-  p.tiles_m = (int)ragged_tiles_bound(p.rows, p.groups, bm);
-  // the XCD order deals ids in eighths: round the grid up so that every eighth fits
-  const int64_t grid = ((int64_t)p.tiles_m * p.tiles_n + 7) / 8 * 8;
-  if (grid == 0) return hipSuccess;
-  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
-  if (bm == 256 && bn == 256) return launch_grouped_tile<256, 2>(p, in, b_layout, out, (unsigned)grid, stream);
-  if (bm == 128 && bn == 128) return launch_grouped_tile<128, 2>(p, in, b_layout, out, (unsigned)grid, stream);
-  if (bm == 64 && bn == 64) return launch_grouped_tile<64, 3>(p, in, b_layout, out, (unsigned)grid, stream);
+hipError_t launch_grouped(GroupedParams p, const TileChoice& c, int in, int b_layout, int out, hipStream_t stream) {
+  p.tiles_m = (int)c.tiles_m;
+  p.tiles_n = (int)c.tiles_n;
+  const unsigned grid = (unsigned)c.grid;
+  if (c.bm == 256) return launch_grouped_tile<256, 2>(p, in, b_layout, out, grid, stream);
+  if (c.bm == 128) return launch_grouped_tile<128, 2>(p, in, b_layout, out, grid, stream);
+  if (c.bm == 64) return launch_grouped_tile<64, 3>(p, in, b_layout, out, grid, stream);
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_wgrad(GroupedParams p, int bm, int bn, int in, int out, hipStream_t stream) {
-  p.tiles_m = (p.M + bm - 1) / bm;
-  p.tiles_n = (p.N + bn - 1) / bn;
-  const int64_t per_group = (int64_t)p.tiles_m * p.tiles_n;
-  if (per_group == 0 || p.groups == 0) return hipSuccess;
-  p.per_xcd = per_group > 8 ? (int)(per_group / 8) : 1;
+hipError_t launch_wgrad(GroupedParams p, const TileChoice& c, int in, int out, hipStream_t stream) {
+  p.tiles_m = (int)c.tiles_m;
+  p.tiles_n = (int)c.tiles_n;
+  p.per_xcd = (int)c.per_xcd;
   p.by_rows = p.groups > 1 && p.groups <= 64 && p.rows >= 256 * p.groups;
-  const int64_t round = 8ll * p.per_xcd, grid = (per_group * p.groups + round - 1) / round * round;
-  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
-  if (bm == 256 && bn == 256) return launch_wgrad_tile<256, 2>(p, in, out, (unsigned)grid, stream);
-  if (bm == 128 && bn == 128) return launch_wgrad_tile<128, 2>(p, in, out, (unsigned)grid, stream);
-  if (bm == 64 && bn == 64) return launch_wgrad_tile<64, 3>(p, in, out, (unsigned)grid, stream);
+  const unsigned grid = (unsigned)c.grid;
+  if (c.bm == 256) return launch_wgrad_tile<256, 2>(p, in, out, grid, stream);
+  if (c.bm == 128) return launch_wgrad_tile<128, 2>(p, in, out, grid, stream);
+  if (c.bm == 64) return launch_wgrad_tile<64, 3>(p, in, out, grid, stream);
   return hipErrorInvalidValue;
 }
 

@@ -16,17 +16,13 @@ static hipError_t launch_rows(const Mx4GemmParams& p, int out, unsigned grid, hi
   return hipGetLastError();
 }
 
-hipError_t launch_few_rows(Mx4GemmParams p, int fmt, int out, hipStream_t stream) {
-  p.g.tiles_n = (p.g.N + 15) / 16;
-  p.g.tiles_m = p.g.offsets ? (int)ragged_tiles_bound(p.g.rows, p.g.groups, 16) : 1;
-  int64_t grid = (int64_t)p.g.tiles_m * p.g.tiles_n;
-  if (p.g.offsets) grid = (grid + 7) / 8 * 8;
-  else if (p.g.rows > 16) return hipErrorInvalidValue;
-  if (grid == 0 || p.g.rows == 0) return hipSuccess;
-  if (grid > kMaxGrid) return hipErrorInvalidConfiguration;
-  if (fmt == kRowsBf16) return launch_rows<kRowsBf16, 1>(p, out, (unsigned)grid, stream);
-  if (fmt == kRowsF16) return launch_rows<kRowsF16, 2>(p, out, (unsigned)grid, stream);
-  return launch_rows<kRowsMx4, 1>(p, out, (unsigned)grid, stream);
+hipError_t launch_few_rows(Mx4GemmParams p, const TileChoice& c, int fmt, int out, hipStream_t stream) {
+  p.g.tiles_m = (int)c.tiles_m;
+  p.g.tiles_n = (int)c.tiles_n;
+  const unsigned grid = (unsigned)c.grid;
+  if (fmt == kRowsBf16) return launch_rows<kRowsBf16, 1>(p, out, grid, stream);
+  if (fmt == kRowsF16) return launch_rows<kRowsF16, 2>(p, out, grid, stream);
+  return launch_rows<kRowsMx4, 1>(p, out, grid, stream);
 }
 
 }  // namespace tbg

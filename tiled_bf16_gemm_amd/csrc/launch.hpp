@@ -5,6 +5,7 @@
 
 #include "fast_div.hpp"
 #include "tbg_desc.hpp"
+#include "tile_choice.hpp"
 
 namespace tbg {
 
@@ -134,17 +135,9 @@ struct GroupedParams {
   int scaled;
 };
 // in: 0 bf16, 1 fp16; out: 0 fp32, 1 bf16, 2 fp16 (a 16-bit output has the input's type).  Tiles
-// 256×256, 128×128, 64×64; they fill the tile counts and the grid.
-hipError_t launch_grouped(GroupedParams p, int bm, int bn, int in, int b_layout, int out, hipStream_t stream);
-hipError_t launch_wgrad(GroupedParams p, int bm, int bn, int in, int out, hipStream_t stream);
-// Workgroups one launch takes: it counts its threads (256 a workgroup) in 32 bits.  The launchers of the
-// ragged and the 4-bit products return hipErrorInvalidConfiguration for more.
-constexpr int64_t kMaxGrid = (1 << 24) - 1;
-// Upper bound of the tiles of height bm over any split of `rows` rows into `groups` groups.
-inline int64_t ragged_tiles_bound(int64_t rows, int64_t groups, int64_t bm) {
-  const int64_t g = groups < rows ? groups : rows;
-  return (rows + g * (bm - 1)) / bm;
-}
+// 256×256, 128×128, 64×64; the launchers fill the tile counts from a choice that fits().
+hipError_t launch_grouped(GroupedParams p, const TileChoice& c, int in, int b_layout, int out, hipStream_t stream);
+hipError_t launch_wgrad(GroupedParams p, const TileChoice& c, int in, int out, hipStream_t stream);
 
 // Arguments of the 4-bit conversions (mx4_quantize.hip): pitches in bytes; per_row = 4 units of 8
 // values for every block of 32 (ceil(cols / 32) blocks); units and div are filled by the launcher.
@@ -168,12 +161,12 @@ struct Mx4GemmParams {
   const uint8_t* Bs;
   int64_t ld_as, ld_bs, stride_bs;
 };
-// Tiles 256×256 (a workgroup for each of `cus` walks them) and 128×128 with 2 stages, 64×64 and 32×64
-// with 2 or 4.
-hipError_t launch_mx4_gemm(Mx4GemmParams p, int bm, int bn, int stages, int out_bf16, int cus, hipStream_t stream);
+// Tiles 256×256 (a workgroup for each CU walks them) and 128×128 with 2 stages, 64×64 and 32×64 with
+// 2 or 4.
+hipError_t launch_mx4_gemm(Mx4GemmParams p, const TileChoice& c, int out_bf16, hipStream_t stream);
 // Products with few rows (gemm_rows.hpp), B stored N×K, at most 16 rows when dense; fmt 0 bf16, 1
 // fp16 (A, B and their pitches as GroupedParams), 2 microscaled 4-bit; out as launch_grouped.
-hipError_t launch_few_rows(Mx4GemmParams p, int fmt, int out, hipStream_t stream);
+hipError_t launch_few_rows(Mx4GemmParams p, const TileChoice& c, int fmt, int out, hipStream_t stream);
 
 // fp8 GEMM (gemm_fp8.hpp): p in units of two fp8 values (lda, ldb, K, kchunks as for 16-bit data
 // of half the width); fmt 0 E4M3, 1 E5M2; tiles 256×256, 128×128, 64×64.
