@@ -691,3 +691,21 @@ def test_a_refused_call_enqueues_nothing():
     assert e.value.status == tbg.ERR_UNSUPPORTED, e.value
     torch.cuda.synchronize()
     assert all((part == 0x5A5A5A5A).all() for part in ws.split(1 << 26))
+
+
+@gpu
+def test_repacks_of_more_than_64_gib_together():
+    """Rows of 1025 values, 16.7 million of them: both operands of the weight gradient are repacked, 32 GiB
+    each, more than the chunks that one launch numbers.  The groups are a few rows at the far end."""
+    M, P, dt, gen = (1 << 24) + 5, 1025, torch.bfloat16, _gen(91)
+    edges = [M - 200, M - 150, M - 150, M - 3]
+    X, Y = (torch.empty((M, P), dtype=dt, device="cuda") for _ in range(2))
+    for t in (X, Y):
+        t[M - 300:] = _ints(gen, (300, P), dt)
+    need = tbg.gemm_grouped_wgrad_workspace_query(3, M, P, P, "bf16", X.data_ptr(), P, Y.data_ptr(), P)
+    assert need > 64 << 30
+    out = _ops().gemm_grouped_wgrad(X, Y, _dev(edges), workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    far = slice(M - 300, M)
+    assert torch.equal(out.double(), _ref_wgrad(X[far], Y[far], [e - (M - 300) for e in edges]))
+    del X, Y
+    torch.cuda.empty_cache()

@@ -92,6 +92,11 @@ int main() {
   CHECK(c.bm == 256 && c.grid == most + 1 && !c.fits(), "tile %d grid %lld", c.bm, (long long)c.grid);
   c = choose_wgrad(4096, up, up, up, 256);
   CHECK(!c.fits(), "grid %lld", (long long)c.grid);
+  // both repacks of a call: 2^24 - 1 workgroups of 256 chunks together, and one chunk more
+  const uint64_t all = (uint64_t)most * 256;
+  CHECK(one_pack_launch(all, 0) && one_pack_launch(0, all) && one_pack_launch(all - 512, 257), "the most");
+  CHECK(!one_pack_launch(all + 1, 0) && !one_pack_launch(all, 1) && !one_pack_launch(all - 512, 513), "one more");
+  CHECK(!one_pack_launch(all / 2 + 256, all / 2 + 256) && !one_pack_launch(~0ull / 4, ~0ull / 4), "far more");
   std::printf("%d problems\n", bad);
   return bad != 0;
 }

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(PackJob j0, PackJob j1, 
   *(uint4*)(j.dst + (uint64_t)r * (uint64_t)j.ld_dst + c * 16u) = pack_chunk(j, r, c * 16u);
 }
 
-// The same for repacks of 2^32 - 256 chunks (64 GiB) or more: 64-bit chunk numbers, numbered flat
+// The same for repacks of more than 2^32 - 256 chunks (64 GiB) together: 64-bit chunk numbers, numbered flat
 // over both repacks, the grid stepping through them.
 __global__ void __launch_bounds__(256) pack_rows_wide_kernel(PackJob j0, PackJob j1, uint64_t n0, uint64_t total,
                                                              uint32_t cpr0, uint32_t cpr1) {
@@ -98,8 +98,7 @@ hipError_t launch_pack_jobs(const PackJob* jobs, int n, hipStream_t stream) {
   }
   const PackJob& j1 = n > 1 ? jobs[1] : jobs[0];
   if (chunks[0] + chunks[1] == 0) return hipSuccess;
-  const uint64_t limit = (1ull << 32) - 256;
-  if (chunks[0] < limit && chunks[1] < limit) {
+  if (one_pack_launch(chunks[0], chunks[1])) {
     const PackGrid g{(uint32_t)chunks[0], (uint32_t)chunks[1], cpr[0], cpr[1], make_fast_div(cpr[0]),
                      make_fast_div(cpr[1])};
     const uint64_t blocks = (chunks[0] + 255) / 256 + (chunks[1] + 255) / 256;

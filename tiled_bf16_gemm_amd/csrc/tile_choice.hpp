@@ -10,6 +10,13 @@ namespace tbg {
 // Workgroups one launch takes: it counts its threads (256 a workgroup) in 32 bits.
 constexpr int64_t kMaxGrid = (1 << 24) - 1;
 
+// Whether one launch of a chunk a thread, 256 to a workgroup, takes both repacks of a call (0 chunks:
+// there is none) and numbers each one's chunks in 32 bits.
+inline bool one_pack_launch(uint64_t chunks0, uint64_t chunks1) {
+  const uint64_t most = (uint64_t)kMaxGrid * 256;
+  return chunks0 <= most && chunks1 <= most && (chunks0 + 255) / 256 + (chunks1 + 255) / 256 <= (uint64_t)kMaxGrid;
+}
+
 // Upper bound of the tiles of height bm over any split of `rows` rows into `groups` groups.
 inline int64_t ragged_tiles_bound(int64_t rows, int64_t groups, int64_t bm) {
   const int64_t g = groups < rows ? groups : rows;
