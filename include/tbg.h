@@ -521,14 +521,16 @@ tbg_status tbg_gemm_grouped_wgrad(int64_t groups, int64_t M, int64_t P, int64_t 
 tbg_status tbg_mx4_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, tbg_dtype x_dtype, void* codes,
                             int64_t ld_codes, void* scales, int64_t ld_scales, void* stream);
 
-/* The values of the first cols columns, written to X (rounded to X's type where it cannot hold
- * them).  Arguments and errors as tbg_mx4_quantize. */
+/* The values of the first cols columns, written to X, rounded once to nearest even: fp32 and bf16 hold
+ * them exactly, subnormal ones included, but for those from 2^128 on (infinity); fp16 rounds to its
+ * subnormals, signed zeros and infinity.  Arguments and errors as tbg_mx4_quantize. */
 tbg_status tbg_mx4_dequantize(int64_t rows, int64_t cols, const void* codes, int64_t ld_codes, const void* scales,
                               int64_t ld_scales, void* X, int64_t ldx, tbg_dtype x_dtype, void* stream);
 
 /* C <- alpha·A·Bᵀ + beta·C for 4-bit A (M×K) and B (stored N×K) on the scaled matrix instruction,
  * fp32 accumulation, C TBG_F32 or TBG_BF16 (row-major, ldc >= N).  alpha, beta as tbg_gemm_ex.  K is
- * a multiple of 32 (columns that quantisation added are zeros and change nothing).
+ * a multiple of 32 (columns that quantisation added are zeros and change nothing).  Scales multiply
+ * together before a term is formed: 2^-127 against 2^127 gives the codes' own product.
  * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.  Limits: sizes up to 2^30, pitches of codes and
  * scales below 2^23 bytes, workgroups as for the ragged products (the largest tiles have no such
  * limit).

@@ -595,3 +595,55 @@ def test_rows_without_a_column():
     off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
     out = ops.mx4_gemm_grouped(a, sa, b, sb, off, "f32", out=torch.full((5, 7), 3.0, device="cuda"), beta=2.0)
     assert (out[:4] == 6).all() and (out[4] == 3).all()
+
+
+def _all_codes():
+    """Every code under every scale byte: codes (256, 16 bytes), scale bytes (256, 1), the values."""
+    code = np.tile(np.arange(32, dtype=np.uint8) % 16, (256, 1))
+    scale = np.arange(256, dtype=np.uint8)[:, None]
+    held = np.zeros((256, 16), dtype=np.uint8)
+    held[:, :1] = scale
+    return torch.from_numpy(pack(code)).cuda(), torch.from_numpy(held).cuda()[:, :1], ref_values(code, scale)
+
+
+@gpu
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16", "f16"])
+def test_every_code_under_every_scale_decodes_to_the_value_rounded_once(out_dtype):
+    """The format's ends included: subnormal values of fp32, bf16 and fp16, values that fp16 rounds (to a
+    subnormal, to zero with its sign) and those past its largest (infinity, as rounding gives)."""
+    codes, scales, want = _all_codes()
+    got = _ops().mx4_dequantize(codes, scales, out_dtype=out_dtype).cpu()
+    assert got[255].isnan().all()
+    # (two significant bits: fp32 and bf16 hold every value below 2^128 exactly)
+    with np.errstate(over="ignore"):
+        w = torch.from_numpy(want[:255].astype(np.float16 if out_dtype == "f16" else np.float32)).to(TORCH[out_dtype])
+    bits = torch.int32 if out_dtype == "f32" else torch.int16
+    bad = (got[:255].view(bits) != w.view(bits)).nonzero()
+    assert len(bad) == 0, [(int(r), int(c), got[r, c].item(), w[r, c].item()) for r, c in bad[:8]]
+
+
+# one size for each kernel of the product (test_grouped_handoff.py checks the choice for such sizes)
+ENDS = [(3, 300, 2080), (20, 300, 2080), (70, 300, 2080), (2000, 2000, 2080), (4000, 4000, 4128)]
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", ENDS)
+def test_product_of_scales_at_the_ends_of_the_format(M, N, K):
+    """Scales from 2^-127 to 2^127 that cancel block by block: every term is a multiple of 1/4 of at most
+    36, so the sum is exact (144·K quarters < 2^24)."""
+    print(f"mx4 product at the format's ends M={M} N={N} K={K}", flush=True)
+    rng = np.random.default_rng(M)
+    a, sa, _ = _random_mx4(rng, (M,), K, spread=0)
+    b, sb, _ = _random_mx4(rng, (N,), K, spread=0)
+    e = rng.integers(0, 255, K // 32)
+    e[:8] = [0, 254, 1, 253, 2, 252, 127, 128]
+    ca, cb = a.cpu().numpy(), b.cpu().numpy()
+    one = np.full(K // 32, 127, dtype=np.uint8)
+    va = torch.from_numpy(ref_values(unpack(ca), np.broadcast_to(one, (M, K // 32)))).cuda()
+    vb = torch.from_numpy(ref_values(unpack(cb), np.broadcast_to(one, (N, K // 32)))).cuda()
+    sa.copy_(torch.from_numpy(e.astype(np.uint8)).expand(M, -1))
+    sb.copy_(torch.from_numpy((254 - e).astype(np.uint8)).expand(N, -1))
+    want = va @ vb.t().contiguous()
+    for out_dtype in ("f32", "bf16"):
+        out = _ops().mx4_gemm(a, sa, b, sb, out_dtype)
+        assert torch.equal(out, want.to(out.dtype)), out_dtype
