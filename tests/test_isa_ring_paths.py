@@ -5,7 +5,12 @@ Copies.  The hand-counted waits hold only if the copy atoms are the only vector-
 flight from a kernel's first copy to its drain.  The drain is the barrier that waits for vmcnt(0) and
 behind which no path leads to another copy (two-stage rings wait for 0 at every barrier of their loop,
 so the count alone does not tell it).  The kernel that walks several tiles stores one while the next
-one's copies are in flight and is left to tests/test_isa_grouped.py."""
+one's copies are in flight and is left to tests/test_isa_grouped.py.
+
+Products.  A matrix product may read a vector register two wait states after a vector instruction
+wrote it, not before.  The compiler sees to that for its builtins and cannot for products written as
+assembly, so here every product is checked: no vector instruction on any path within two wait
+states (each instruction counts 1, s_nop N counts N + 1) before it may write one of its registers."""
 import concurrent.futures
 import os
 import re
@@ -15,6 +20,8 @@ import pytest
 
 from tests.test_isa_grouped import KERNEL, SOURCES, _is_copy
 from tests.test_isa_hazards import CSRC, INCLUDE, _blocks, _hipcc, _vmcnt
+
+WAIT_STATES = 2
 
 
 def successors(bl):
@@ -70,6 +77,63 @@ def stray_vmem(lines):
     return stray, len(drains)
 
 
+def _vregs(tok):
+    """Vector registers a operand names: v5, a7, v[0:3]."""
+    m = re.match(r"([va])(?:(\d+)|\[(\d+):(\d+)\])$", tok.strip())
+    if not m:
+        return set()
+    lo, hi = (m.group(2), m.group(2)) if m.group(2) else (m.group(3), m.group(4))
+    return {f"{m.group(1)}{r}" for r in range(int(lo), int(hi) + 1)}
+
+
+def _operands(t):
+    rest = re.sub(r"\s(op_sel|op_sel_hi|cbsz|blgp|abid|neg_lo|neg_hi|quad_perm|row_\w+|row_mask|bank_mask|bound_ctrl)\b.*$", "",
+                  t.partition(" ")[2])
+    return [o for o in re.split(r",\s*(?![^\[]*\])", rest)]
+
+
+def _writes(t):
+    """Vector registers a vector instruction other than a product writes."""
+    if not t.startswith("v_") or t.startswith(("v_mfma", "v_cmp", "v_readfirstlane", "v_readlane", "v_nop")):
+        return set()
+    ops = _operands(t)
+    two = t.startswith(("v_swap", "v_permlane16_swap", "v_permlane32_swap"))
+    return _vregs(ops[0]) | (_vregs(ops[1]) if two else set())
+
+
+def early_reads(lines):
+    """(product, vector instruction that wrote one of its registers, wait states between), closer than
+    WAIT_STATES on some path; and the number of products."""
+    bl = _blocks(lines)
+    pred = [[] for _ in bl]
+    for i, nxt in enumerate(successors(bl)):
+        for n in nxt:
+            pred[n].append(i)
+    found, products = [], 0
+
+    def back(i, j, need, states, t, seen):
+        while j > 0 and states < WAIT_STATES:
+            j -= 1
+            p = bl[i][1][j]
+            if _writes(p) & need:
+                found.append((t, p, states))
+                return
+            m = re.match(r"s_nop (\d+)", p)
+            states += int(m.group(1)) + 1 if m else 1
+        if states < WAIT_STATES:
+            for q in pred[i]:
+                if (q, states) not in seen:
+                    seen.add((q, states))
+                    back(q, len(bl[q][1]), need, states, t, seen)
+
+    for i, (_, ins) in enumerate(bl):
+        for j, t in enumerate(ins):
+            if t.startswith("v_mfma"):
+                products += 1
+                back(i, j, set().union(*map(_vregs, _operands(t)[1:])), 0, t, set())
+    return found, products
+
+
 COPY = "buffer_load_dwordx4 v1, s[8:11], 0 offen lds"
 
 
@@ -91,6 +155,20 @@ def test_stray_vmem_on_small_listings():
     assert stray_vmem(laid_out) == ([], 1)
     assert stray_vmem([t if t != "s_branch .LBB0_3" else "s_cbranch_scc0 .LBB0_3" for t in laid_out])[0] == [store, load]
     assert stray_vmem(head + loop + [store, "s_endpgm"]) == ([store], 0)
+
+
+def test_early_reads_on_small_listings():
+    product = "v_mfma_scale_f32_16x16x128_f8f6f4 a[0:3], v[4:7], v[8:11], a[0:3], v12, v13 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+    assert early_reads(["v_and_b32_e32 v12, v1, v2", product])[0] == [(product, "v_and_b32_e32 v12, v1, v2", 0)]
+    assert early_reads(["v_and_b32_e32 v13, v1, v2", "s_nop 0", product])[0][0][2] == 1
+    assert early_reads(["v_mov_b64_e32 v[6:7], v[2:3]", "s_mov_b32 s1, s2", product])[0][0][2] == 1
+    assert early_reads(["v_accvgpr_write_b32 a2, 0", product])[0][0][2] == 0
+    assert early_reads(["v_swap_b32 v1, v12", product])[0][0][2] == 0
+    for far in (["v_and_b32_e32 v12, v1, v2", "s_nop 1"], ["v_and_b32_e32 v12, v1, v2", "s_nop 0", "s_mov_b32 s1, s2"],
+                ["v_and_b32_e32 v14, v12, v13"], ["v_cmp_lt_i32_e32 vcc, v12, v13"], ["v_readfirstlane_b32 s12, v12"]):
+        assert early_reads(far + [product]) == ([], 1)
+    looped = [".LBB0_1:", product, "v_add_u32_e32 v9, 1, v9", "s_cbranch_scc1 .LBB0_1", "s_endpgm"]
+    assert early_reads(looped)[0] == [(product, "v_add_u32_e32 v9, 1, v9", 1)]
 
 
 def _listing(src, tmp):
@@ -126,4 +204,13 @@ def test_only_copies_are_in_flight_up_to_the_drain(kernels):
             stray, drains = stray_vmem(lines)
             if stray or not drains:
                 problems.append(f"{name}: {stray[:3]} among the copies, {drains} drains")
+    assert not problems, "\n".join(problems[:20])
+
+
+def test_no_product_reads_a_register_that_was_just_written(kernels):
+    problems = []
+    for name, lines in kernels:
+        found, products = early_reads(lines)
+        assert products, name
+        problems += [f"{name}: {t!r} {n} wait states after {p!r}" for t, p, n in found[:2]]
     assert not problems, "\n".join(problems[:20])

@@ -209,9 +209,9 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], con
     const uint8_t* buf = scales + (quad & 1) * C::QuadBytes + lane_s + ((QT >> 1) ^ swap) * 16 + (QT & 1) * 8;
     s[i] = *(const uint16_t*)(buf + (i < FM ? wm * T::TM * 32 + i * 512 : (T::BM + wn * T::TN) * 32 + (i - FM) * 512));
   };
-  // Zero the bytes of blocks past the end.  The empty statement keeps the masking next to the
-  // reads: products written as assembly must not follow a vector instruction that writes their
-  // operand directly.
+  // Zero the bytes of blocks past the end.  A product may read a register two wait states after a vector
+  // instruction wrote it, which the compiler does not see to for products written as assembly: the
+  // empty statements, the wait and those products are all volatile, so they stay in this order.
   auto mask_scales = [&](uint32_t (&s)[R], int kt) __attribute__((always_inline)) {
     const int left = blocks - kt * 8 - 2 * pair;
     const uint32_t keep = left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
@@ -220,6 +220,7 @@ __device__ __forceinline__ void mx4_ring(f32x4_t (&acc)[C::T::FN][C::T::FM], con
       s[i] &= keep;
       asm volatile("" : "+v"(s[i]));
     }
+    if (T::AsmMfma) asm volatile("s_nop 1");
   };
 
   // One k-step: KK says which blocks the products take; the fragments of the other k-step are
