@@ -16,7 +16,6 @@
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <type_traits>
 
 #include "launch.hpp"
 
@@ -75,6 +74,12 @@ struct RaggedTile {
   int tn;    // tile column
 };
 
+// Tiles of BM rows that hold `rows` (never negative) rows.
+template <int BM>
+__device__ __forceinline__ int tile_rows(int rows) {
+  return (int)(((uint32_t)rows + BM - 1) / BM);
+}
+
 // Tiles of BM rows over the groups, and each lane's share of them.
 struct RaggedPlan {
   int upto, mine;  // tile rows up to and with this lane's groups; in them
@@ -88,22 +93,24 @@ __device__ __forceinline__ RaggedPlan ragged_plan(const int32_t* offsets, int gr
   const int per = (groups + 63) >> 6, g0 = (threadIdx.x & 63) * per;
   RaggedPlan p;
   p.least = 0;
-  bool descends = false;
-  auto count = [&](auto first) __attribute__((always_inline)) {
+  // Lanes that met a descending pair: a scalar, as all lanes stay active (one without a group looks at
+  // the last).  With the lanes' own flags and a branch a lane, 4 rows of 4 groups in 4 bits took 2.99 µs
+  // against 2.85.
+  uint64_t descends = 0;
+  auto count = [&] {
     p.mine = p.begin = 0;
     p.end = p.least;
     for (int j = 0; j < per; ++j) {
-      if (g0 + j < groups) {
-        if (decltype(first)::value) descends |= offsets[g0 + j + 1] < offsets[g0 + j];
-        group_rows(offsets, g0 + j, p.end, rows, p.begin, p.end);
-        p.mine += (p.end - p.begin + BM - 1) / BM;
-      }
+      const int g = min(g0 + j, groups - 1);
+      descends |= __ballot(offsets[g + 1] < offsets[g]);
+      group_rows(offsets, g, p.end, rows, p.begin, p.end);
+      p.mine += g0 + j < groups ? tile_rows<BM>(p.end - p.begin) : 0;
     }
   };
-  count(std::true_type{});
-  if (__ballot(descends) != 0) {
+  count();
+  if (__builtin_expect(descends != 0, 0)) {
     p.least = wave_max_before(p.end);
-    count(std::false_type{});
+    count();
   }
   p.upto = wave_prefix_sum(p.mine);
   p.tiles = __builtin_amdgcn_readlane(p.upto, 63) * tiles_n;
@@ -121,7 +128,7 @@ __device__ __forceinline__ void ragged_find(const RaggedPlan& p, const int32_t* 
   for (int j = 0; j < per; ++j) {
     if (g0 + j < groups) {
       if (per > 1) group_rows(offsets, g0 + j, end, rows, begin, end);
-      const int n = (end - begin + BM - 1) / BM * tiles_n;
+      const int n = tile_rows<BM>(end - begin) * tiles_n;
       if (lid >= at && lid < at + n) {
         found = g0 + j;
         fb = begin;
@@ -135,7 +142,7 @@ __device__ __forceinline__ void ragged_find(const RaggedPlan& p, const int32_t* 
   t.group = __builtin_amdgcn_readlane(found, src);
   const int b = __builtin_amdgcn_readlane(fb, src), e = __builtin_amdgcn_readlane(fe, src);
   int tm;
-  band_tile(__builtin_amdgcn_readlane(fi, src), (e - b + BM - 1) / BM, tiles_n, height, tm, t.tn);
+  band_tile(__builtin_amdgcn_readlane(fi, src), tile_rows<BM>(e - b), tiles_n, height, tm, t.tn);
   t.row0 = b + tm * BM;
   t.rows = e - t.row0;
 }
