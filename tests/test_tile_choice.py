@@ -78,6 +78,12 @@ int main() {
     c = choose_mx4(1, M, 64 * (most - 7) + 1, 32, 256);
     CHECK(c.grid == most + 1 && !c.fits(), "M %lld grid %lld", (long long)M, (long long)c.grid);
   }
+  // stages of the 64-column tiles: up to 1.5 workgroups a compute unit, and from K = 8192 on
+  for (int64_t M : {20, 60}) {
+    CHECK(choose_mx4(0, M, 64 * 384, 4096, 256).stages == 4 && choose_mx4(0, M, 64 * 385, 4096, 256).stages == 2, "M %d", (int)M);
+    CHECK(choose_mx4(0, M, 64 * 4000, 8160, 256).stages == 2 && choose_mx4(0, M, 64 * 4000, 8192, 256).stages == 4, "M %d", (int)M);
+    CHECK(choose_mx4(16, 16 * M, 64 * 24, 4096, 256).stages == 4 && choose_mx4(16, 16 * M, 64 * 25, 4096, 256).stages == 2, "M %d", (int)M);
+  }
   // the walking tile: any number of tiles that 32 bits hold, on as many workgroups as compute units
   for (int64_t groups : {0, 3}) {
     TileChoice c = choose_mx4(groups, 1 << 22, 1 << 22, 8192, 256);

@@ -138,10 +138,7 @@ inline TileChoice choose_mx4(int64_t groups, int64_t M, int64_t N, int64_t K, in
   const double active = ragged ? (double)(groups < M ? groups : M) : 1.0;
   c.few = takes_few_rows(active, (double)M, N, cus) && (ragged || M <= 16);
   // Up to 32 rows a group: 32-row tiles, which copy half as many masked rows of A as 64-row ones (40
-  // groups of one or two rows, N = 4096, K = 2048: 34.7 against 40.0 µs).  Two stages instead of four
-  // let more workgroups share a CU, which pays once there are enough of them (the same product
-  // 34.7 against 40.4 µs); few workgroups need the depth (N = 8192, K = 8192, one row: 17.6 against
-  // 10.0 µs).
+  // groups of one or two rows, N = 4096, K = 2048: 34.7 against 40.0 µs).
   c.stages = 2;
   if (c.few) {
     c.bm = c.bn = 16;
@@ -152,8 +149,17 @@ inline TileChoice choose_mx4(int64_t groups, int64_t M, int64_t N, int64_t K, in
   } else {
     c.bm = c.bn = choose_rows_tile(kTiles4, active, (double)M, N, ceil((double)K / 256), cus);
   }
-  if (c.bn == 64 && narrow_tiles(active, N) * ((double)M / active > c.bm ? (double)M / active / c.bm : 1) < 4 * cus)
-    c.stages = 4;
+  // The tiles of 64 columns have rings of two and of four stages.  Two take less LDS, so more workgroups
+  // share a CU and hide each other's copies; up to 1.5 workgroups a CU there are no others, and over a
+  // long K the depth pays whatever their number.  2 against 4 stages in µs, 20 rows, by workgroups a CU:
+  //   K = 2048   1: 7.6, 6.7    1.5: 8.7, 8.8     2: 9.4, 9.6     4: 14.3, 15.6   10: 38.0, 41.6
+  //   K = 4096   1: 11.6, 9.6   1.5: 12.4, 12.3   2: 13.9, 14.2   4: 29.9, 31.1   10: 69.9, 69.5
+  //   K = 8192   1: 18.6, 14.3  1.5: 26.6, 22.8   2: 37.1, 33.2   4: 68.9, 61.1   10: 132, 122
+  // (60 rows, and 16 groups of 10 or 50, alike; between K = 4096 and 8192 either may lead by a tenth)
+  if (c.bn == 64) {
+    const double tall = (double)M / active / c.bm, workgroups = narrow_tiles(active, N) * (tall > 1 ? tall : 1);
+    if (workgroups <= 1.5 * cus || K >= 8192) c.stages = 4;
+  }
   c.walks = c.bm == 256;
   set_row_tiles(c, groups, M, N);
   if (c.walks) {
