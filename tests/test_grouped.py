@@ -709,3 +709,21 @@ def test_repacks_of_more_than_64_gib_together():
     assert torch.equal(out.double(), _ref_wgrad(X[far], Y[far], [e - (M - 300) for e in edges]))
     del X, Y
     torch.cuda.empty_cache()
+
+
+@gpu
+@pytest.mark.parametrize("groups,dtype", [(64, "bf16"), (64, "f16"), (5, "bf16"), (2, "f16")])
+def test_wgrad_exact_in_the_order_of_the_rows(groups, dtype):
+    """1024 rows a group on average, up to 64 groups: the groups run longest first.  Equal ones, empty ones
+    and one of most of the rows."""
+    sizes = ([900, 0, 1100, 900] * groups)[:groups]
+    sizes[groups // 2] += 1024 * groups - sum(sizes) + 8
+    edges, P, Q, dt = _offsets(sizes, 3), 137, 72, TORCH[dtype]
+    M, gen = edges[-1] + 5, _gen(groups)
+    X, Y = _ints(gen, (M, P), dt), _ints(gen, (M, Q), dt)
+    want = _ref_wgrad(X, Y, edges)
+    for t in (X, Y):
+        t[:3], t[edges[-1]:] = float("nan"), float("nan")
+    out = torch.full((groups, P, Q), float("nan"), device="cuda")
+    _ops().gemm_grouped_wgrad(X, Y, _dev(edges), out=out)
+    assert torch.equal(out.double(), want)

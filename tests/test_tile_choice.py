@@ -98,6 +98,10 @@ int main() {
   CHECK(c.bm == 256 && c.grid == most + 1 && !c.fits(), "tile %d grid %lld", c.bm, (long long)c.grid);
   c = choose_wgrad(4096, up, up, up, 256);
   CHECK(!c.fits(), "grid %lld", (long long)c.grid);
+  // groups in the order of their rows: 2 to 64 of 1024 rows on average
+  CHECK(choose_wgrad(64, 65536, 99, 99, 256).by_rows && choose_wgrad(2, 2048, 99, 99, 256).by_rows, "by rows");
+  CHECK(!choose_wgrad(64, 65535, 99, 99, 256).by_rows && !choose_wgrad(65, 1 << 20, 99, 99, 256).by_rows, "by number");
+  CHECK(!choose_wgrad(1, 1 << 20, 99, 99, 256).by_rows, "one group");
   // both repacks of a call: 2^24 - 1 workgroups of 256 chunks together, and one chunk more
   const uint64_t all = (uint64_t)most * 256;
   CHECK(one_pack_launch(all, 0) && one_pack_launch(0, all) && one_pack_launch(all - 512, 257), "the most");

@@ -26,7 +26,7 @@ hipError_t launch_wgrad(GroupedParams p, const TileChoice& c, int in, int out, h
   p.tiles_m = (int)c.tiles_m;
   p.tiles_n = (int)c.tiles_n;
   p.per_xcd = (int)c.per_xcd;
-  p.by_rows = p.groups > 1 && p.groups <= 64 && p.rows >= 256 * p.groups;
+  p.by_rows = c.by_rows ? 1 : 0;
   const unsigned grid = (unsigned)c.grid;
   if (c.bm == 256) return launch_wgrad_tile<256, 2>(p, in, out, grid, stream);
   if (c.bm == 128) return launch_wgrad_tile<128, 2>(p, in, out, grid, stream);
