@@ -42,7 +42,8 @@ __device__ __forceinline__ void load_piece(RowsPiece<FMT>& p, const uint8_t* row
   if (FMT == kRowsMx4) p.s = *(const u32x4_t*)(scales + (int64_t)chunk * 16);
 }
 
-// The last chunk of a row when it is not whole: `left` bytes remain in it, a multiple of 16.
+// The last chunk of a row when it is not whole: `left` bytes remain in it, a multiple of 16 in 4 bits; in
+// 16 bits a repack has filled the last 16 bytes with zeros.
 template <int FMT>
 __device__ __forceinline__ void load_piece_end(RowsPiece<FMT>& p, const uint8_t* row, const uint8_t* scales, int chunk,
                                                int left, int g) {

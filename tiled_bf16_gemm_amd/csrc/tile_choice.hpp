@@ -46,7 +46,9 @@ inline int64_t whole_eighths(int64_t n) { return (n + 7) / 8 * 8; }
 // The figures are fitted to every tile's time on thousands of shapes (MI355X, 4 to 64 groups of 70 to
 // 2048 rows on average, N of 256 to 14336, K of 256 to 8192; the 4-bit ones also dense): the tile
 // chosen takes 1.0 % (16-bit rows), 1.4 % (weight gradient) and 0.9 % (4 bits) longer than the
-// best one on average.
+// best one on average.  Outside that range (one to three groups, 8 to 69 rows a group, widths off 64;
+// 249 shapes, either layout of B) it takes up to 1.7 % longer on average, 23 % at worst, but the times
+// are no prediction there (31 groups of 258 rows, K×N at a pitch of 4000 bytes, K = 1001: 71 µs for 50).
 struct TileTime {
   int b, per_cu;
   double fixed, per, part;
