@@ -95,7 +95,7 @@ def draw(rng):
                     group=group, zeros=rng.random() < 0.5, dtype=dtype, out=rng.choice([dtype, "f32"]),
                     gather=rng.random() < 0.5)
     case = dict(op=op, **_routing(rng, 8192, 128), H=_spread(rng, 16, 8192), dtype=rng.choice(["bf16", "f16", "f32"]))
-    while case["tokens"] * case["top_k"] * case["H"] > 8192 * 2 * 4096:
+    while case["tokens"] * case["top_k"] * case["H"] * SIZE[case["dtype"]] > 8192 * 2 * 4096 * 2:
         case["H"] = max(16, case["H"] // 2)
     if op != "dispatch":
         case["out"] = rng.choice(["f32", case["dtype"]])
