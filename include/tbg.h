@@ -548,6 +548,109 @@ tbg_status tbg_mx4_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K,
                                 int64_t ldb, int64_t stride_b, const void* B_scales, int64_t ld_bs, int64_t stride_bs,
                                 float beta, void* C, int64_t ldc, tbg_dtype c_dtype, void* stream);
 
+/* ---- tokens by expert --------------------------------------------------------------------------
+ * What stands around the ragged products.  A router gives each of T tokens k choices among `groups`
+ * experts: n = T*k slots, slot t*k + j being choice j of token t.  Sorted by expert the slots become the
+ * rows of the groups; `place` says which row a slot became, `source` which slot a row came from.  All of
+ * it is device memory read when the work runs, so a captured graph replays with new choices. */
+
+/* Workspace bytes tbg_expert_sort needs: 0 up to 4096 slots, above that the counts of up to 256 parts of
+ * the slots by expert.  0 for sizes the call refuses. */
+size_t tbg_expert_sort_workspace_query(int64_t slots, int64_t groups);
+
+/* A stable sort of the slots by expert.
+ *   experts   int32, one per slot.  Values outside 0..groups-1 (padded or dropped) belong to no expert.
+ *   offsets   int32, groups + 1 values: group e holds rows offsets[e] .. offsets[e+1]-1, offsets[0] = 0.
+ *   source    int32, one per row: its slot; within a group the slots ascend.  Rows from offsets[groups] on
+ *             get -1.
+ *   place     int32, one per slot: its row, or -1 for a slot of no expert.
+ * The arrays are 4-byte aligned and must not overlap.  Calls that may run at once need a workspace (256-byte
+ * aligned; NULL when none is needed) each.  slots == 0 gives zero offsets.
+ * Limits: slots up to 2^30, groups up to 4096.
+ * Returns INVALID_VALUE (negative sizes, null pointers), MISALIGNED, UNSUPPORTED (limits), OUT_OF_RANGE
+ * (workspace too small), NO_DEVICE / HIP. */
+tbg_status tbg_expert_sort(int64_t slots, int64_t groups, const int32_t* experts, int32_t* offsets, int32_t* source,
+                           int32_t* place, void* workspace, size_t workspace_bytes, void* stream);
+
+/* out[place[t*top_k + j]] <- X[t] for every choice j of every token t: the rows of the groups.
+ *   X         tokens rows of cols elements (any type: they are copied), ldx >= cols.
+ *   place     int32, tokens*top_k values, as tbg_expert_sort gives them.  Values outside 0..rows-1 are no
+ *             row.  Rows that no slot holds are left as they were; of slots that hold the same row
+ *             (tbg_expert_sort makes none) either one's token is written.
+ *   out       rows rows of the same type, ld_out >= cols; must not overlap X or place.
+ * Any alignment of whole elements.  Codes and scales of microscaled 4-bit rows are matrices of TBG_U8.
+ * The gradient of X is tbg_expert_combine of out's without weights.
+ * tokens, top_k, cols or rows == 0 is a no-op.
+ * Limits: tokens*top_k and rows up to 2^30, top_k up to 1024, cols up to 2^30.
+ * Returns INVALID_VALUE (negative sizes, pitches, null pointers, type), MISALIGNED, UNSUPPORTED (limits),
+ * NO_DEVICE / HIP. */
+tbg_status tbg_expert_dispatch(int64_t tokens, int64_t top_k, int64_t rows, int64_t cols, tbg_dtype dtype,
+                               const void* X, int64_t ldx, const int32_t* place, void* out, int64_t ld_out,
+                               void* stream);
+
+/* out[t] <- the sum over j of weights[t*top_k + j] * Y[place[t*top_k + j]]: the rows of the groups back at
+ * their tokens.
+ *   Y         rows rows of cols values, TBG_F32, TBG_BF16 or TBG_F16, ldy >= cols.
+ *   place     as tbg_expert_dispatch; a slot without a row adds nothing, whatever its weight.
+ *   weights   fp32, tokens*top_k values, or NULL: every weight 1.
+ *   out       tokens rows, TBG_F32 or Y's type, ld_out >= cols.  The sum is held in fp32, j ascending, and
+ *             rounded once to nearest even; a token without a row gets zeros.
+ * Alignment, limits and errors as tbg_expert_dispatch; out must not overlap the inputs.  tokens or cols == 0
+ * is a no-op. */
+tbg_status tbg_expert_combine(int64_t tokens, int64_t top_k, int64_t rows, int64_t cols, const void* Y, int64_t ldy,
+                              tbg_dtype y_dtype, const int32_t* place, const float* weights, void* out,
+                              int64_t ld_out, tbg_dtype out_dtype, void* stream);
+
+/* The gradients of Y and of the weights under tbg_expert_combine, dout being the gradient of its out:
+ *   dY[place[s]]   <- weights[s] * dout[t], rounded once to Y's type.  Rows that no slot holds are left as
+ *                     they were.
+ *   dweights[s]    <- the sum over the columns of Y[place[s]] * dout[t], held in fp32; 0 for a slot without
+ *                     a row.
+ *   dout           tokens rows, TBG_F32 or Y's type, ldd >= cols.
+ *   dY             rows rows of Y's type, ld_dy >= cols; must not overlap the inputs.
+ *   dweights       fp32, tokens*top_k values.
+ * Every sum has one order for given sizes.  Other arguments, limits and errors as tbg_expert_combine; weights
+ * NULL counts as ones.  tokens or top_k == 0 is a no-op; cols == 0 or rows == 0 gives zero dweights. */
+tbg_status tbg_expert_combine_grad(int64_t tokens, int64_t top_k, int64_t rows, int64_t cols, const void* dout,
+                                   int64_t ldd, tbg_dtype dout_dtype, const void* Y, int64_t ldy, tbg_dtype y_dtype,
+                                   const int32_t* place, const float* weights, void* dY, int64_t ld_dy,
+                                   float* dweights, void* stream);
+
+/* ---- weights in 4-bit codes --------------------------------------------------------------------
+ * A weight matrix of N rows and K columns held as whole numbers 0..15 with a scale, and a zero where it has
+ * one, for every group of `group` columns (32, 64 or 128; K a multiple of it) of a row:
+ *   W[n][k] = scales[k / group][n] * (code[n][k] - zeros[k / group][n])
+ *   codes     two per byte, the lower nibble first: N rows of K/2 bytes, ldb bytes apart; 16-byte aligned,
+ *             ldb a multiple of 16.
+ *   scales    of A's type, K/group rows of N values, ld_s elements apart, 2-byte aligned.
+ *   zeros     one byte each, K/group rows of N, ld_z bytes apart; NULL: every zero is 8. */
+
+/* C <- alpha·A·Wᵀ + beta·C for M rows of activations A (TBG_BF16 or TBG_F16, lda >= K, any alignment of whole
+ * elements) and a weight matrix as above; C TBG_F32 or A's type, ldc >= N.
+ * Per group the sum of A times whole numbers is held in fp32, multiplied by the scale and added in fp32;
+ * nothing else is rounded before C, once, to nearest even.  alpha, beta as tbg_gemm_ex.  Made for few rows
+ * (the bytes of W are the cost); any number is taken.
+ * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.
+ * Limits: M, N, K up to 2^30, ldb below 2^30, workgroups as for the ragged products.
+ * Returns INVALID_VALUE (negative sizes, group, K % group, pitches, null pointers, types), MISALIGNED,
+ * UNSUPPORTED (limits), NO_DEVICE / HIP. */
+tbg_status tbg_w4_gemm(int64_t M, int64_t N, int64_t K, int64_t group, float alpha, const void* A, int64_t lda,
+                       tbg_dtype ab_dtype, const void* codes, int64_t ldb, const void* scales, int64_t ld_s,
+                       const uint8_t* zeros, int64_t ld_z, float beta, void* C, int64_t ldc, tbg_dtype c_dtype,
+                       void* stream);
+
+/* tbg_w4_gemm over ragged groups: C[r] <- alpha·A[r]·W_eᵀ + beta·C[r] for the rows r of group e.  W_e's codes
+ * start stride_b bytes after W_(e-1)'s (a multiple of 16), its scales stride_s elements, its zeros stride_z
+ * bytes after.  offsets, groups and rows of no group as tbg_gemm_grouped.
+ *   source    NULL, or int32, M values, 4-byte aligned: row r reads A[source[r] / top_k] instead of A[r] (the
+ *             rows of tbg_expert_sort without a copy of them).  A then has a_rows rows; an index outside them
+ *             is taken as the nearer one.  Without source, a_rows and top_k are not used. */
+tbg_status tbg_w4_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group, const int32_t* offsets,
+                               const int32_t* source, int64_t a_rows, int64_t top_k, float alpha, const void* A,
+                               int64_t lda, tbg_dtype ab_dtype, const void* codes, int64_t ldb, int64_t stride_b,
+                               const void* scales, int64_t ld_s, int64_t stride_s, const uint8_t* zeros, int64_t ld_z,
+                               int64_t stride_z, float beta, void* C, int64_t ldc, tbg_dtype c_dtype, void* stream);
+
 /* Static text for a status code. */
 const char* tbg_status_string(tbg_status s);
 

@@ -174,6 +174,25 @@ _lib.tbg_mx4_gemm.argtypes = [_i64, _i64, _i64, _f32, _vp, _i64, _vp, _i64, _vp,
 _lib.tbg_mx4_gemm_grouped.restype = ctypes.c_int
 _lib.tbg_mx4_gemm_grouped.argtypes = [_i64, _i64, _i64, _i64, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp,
                                       _i64, _i64, _f32, _vp, _i64, ctypes.c_int, _vp]
+_lib.tbg_expert_sort_workspace_query.restype = ctypes.c_size_t
+_lib.tbg_expert_sort_workspace_query.argtypes = [_i64, _i64]
+_lib.tbg_expert_sort.restype = ctypes.c_int
+_lib.tbg_expert_sort.argtypes = [_i64, _i64, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.tbg_expert_dispatch.restype = ctypes.c_int
+_lib.tbg_expert_dispatch.argtypes = [_i64, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _vp, _i64, _vp]
+_lib.tbg_expert_combine.restype = ctypes.c_int
+_lib.tbg_expert_combine.argtypes = [_i64, _i64, _i64, _i64, _vp, _i64, ctypes.c_int, _vp, _vp, _vp, _i64, ctypes.c_int,
+                                    _vp]
+_lib.tbg_expert_combine_grad.restype = ctypes.c_int
+_lib.tbg_expert_combine_grad.argtypes = [_i64, _i64, _i64, _i64, _vp, _i64, ctypes.c_int, _vp, _i64, ctypes.c_int, _vp,
+                                         _vp, _vp, _i64, _vp, _vp]
+_lib.tbg_w4_gemm.restype = ctypes.c_int
+_lib.tbg_w4_gemm.argtypes = [_i64, _i64, _i64, _i64, _f32, _vp, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _i64,
+                             _f32, _vp, _i64, ctypes.c_int, _vp]
+_lib.tbg_w4_gemm_grouped.restype = ctypes.c_int
+_lib.tbg_w4_gemm_grouped.argtypes = [_i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _i64, ctypes.c_int,
+                                     _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _f32, _vp, _i64, ctypes.c_int,
+                                     _vp]
 _lib.tbg_status_string.restype = ctypes.c_char_p
 _lib.tbg_status_string.argtypes = [ctypes.c_int]
 _lib.tbg_last_error.restype = ctypes.c_char_p
@@ -478,6 +497,59 @@ def mx4_gemm_grouped(groups: int, M: int, N: int, K: int, offsets: int, alpha: f
     _check(_lib.tbg_mx4_gemm_grouped(groups, M, N, K, offsets, alpha, A, lda, A_scales, ld_as,
                                      B, ldb, stride_b, B_scales, ld_bs, stride_bs, beta, C, ldc,
                                      _enum(DTYPES, c_dtype), stream or None))
+
+
+def expert_sort_workspace_query(slots: int, groups: int) -> int:
+    return int(_lib.tbg_expert_sort_workspace_query(slots, groups))
+
+
+def expert_sort(slots: int, groups: int, experts: int, offsets: int, source: int, place: int, workspace: int = 0,
+                workspace_bytes: int = 0, stream: Optional[int] = None) -> None:
+    """tbg_expert_sort: a stable sort of the slots by expert."""
+    _check(_lib.tbg_expert_sort(slots, groups, experts, offsets, source, place, workspace, workspace_bytes,
+                                stream or None))
+
+
+def expert_dispatch(tokens: int, top_k: int, rows: int, cols: int, dtype, X: int, ldx: int, place: int, out: int,
+                    ld_out: int, stream: Optional[int] = None) -> None:
+    """tbg_expert_dispatch: out[place[t*top_k + j]] = X[t]."""
+    _check(_lib.tbg_expert_dispatch(tokens, top_k, rows, cols, _enum(DTYPES, dtype), X, ldx, place, out, ld_out,
+                                    stream or None))
+
+
+def expert_combine(tokens: int, top_k: int, rows: int, cols: int, Y: int, ldy: int, y_dtype, place: int, weights: int,
+                   out: int, ld_out: int, out_dtype, stream: Optional[int] = None) -> None:
+    """tbg_expert_combine: out[t] = sum over j of weights[t*top_k + j] * Y[place[t*top_k + j]] (weights 0: ones)."""
+    _check(_lib.tbg_expert_combine(tokens, top_k, rows, cols, Y, ldy, _enum(DTYPES, y_dtype), place, weights or None, out,
+                                   ld_out, _enum(DTYPES, out_dtype), stream or None))
+
+
+def expert_combine_grad(tokens: int, top_k: int, rows: int, cols: int, dout: int, ldd: int, dout_dtype, Y: int, ldy: int,
+                        y_dtype, place: int, weights: int, dY: int, ld_dy: int, dweights: int,
+                        stream: Optional[int] = None) -> None:
+    """tbg_expert_combine_grad: the gradients of Y and of the weights under tbg_expert_combine."""
+    _check(_lib.tbg_expert_combine_grad(tokens, top_k, rows, cols, dout, ldd, _enum(DTYPES, dout_dtype), Y, ldy,
+                                        _enum(DTYPES, y_dtype), place, weights or None, dY, ld_dy, dweights,
+                                        stream or None))
+
+
+def w4_gemm(M: int, N: int, K: int, group: int, alpha: float, A: int, lda: int, ab_dtype, codes: int, ldb: int,
+            scales: int, ld_s: int, zeros: int, ld_z: int, beta: float, C: int, ldc: int, c_dtype,
+            stream: Optional[int] = None) -> None:
+    """tbg_w4_gemm: C = alpha·A·Wᵀ + beta·C for a W in 4-bit codes (zeros 0: every zero is 8)."""
+    _check(_lib.tbg_w4_gemm(M, N, K, group, alpha, A, lda, _enum(DTYPES, ab_dtype), codes, ldb, scales, ld_s,
+                            zeros or None, ld_z, beta, C, ldc, _enum(DTYPES, c_dtype), stream or None))
+
+
+def w4_gemm_grouped(groups: int, M: int, N: int, K: int, group: int, offsets: int, source: int, a_rows: int, top_k: int,
+                    alpha: float, A: int, lda: int, ab_dtype, codes: int, ldb: int, stride_b: int, scales: int,
+                    ld_s: int, stride_s: int, zeros: int, ld_z: int, stride_z: int, beta: float, C: int, ldc: int,
+                    c_dtype, stream: Optional[int] = None) -> None:
+    """tbg_w4_gemm_grouped: tbg_w4_gemm for the rows of every group with its own W (source 0: rows in order)."""
+    _check(_lib.tbg_w4_gemm_grouped(groups, M, N, K, group, offsets, source or None, a_rows, top_k, alpha, A, lda,
+                                    _enum(DTYPES, ab_dtype), codes, ldb, stride_b, scales, ld_s, stride_s,
+                                    zeros or None, ld_z, stride_z, beta, C, ldc, _enum(DTYPES, c_dtype),
+                                    stream or None))
 
 
 def declared_functions() -> list:

@@ -466,3 +466,116 @@ tbg_status tbg_mx4_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K,
 }
 
 }  // extern "C"
+
+namespace {
+
+// Both products with weights in 4-bit codes: groups < 0 is the dense one.
+tbg_status w4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group, const int32_t* offsets,
+                        const int32_t* source, int64_t a_rows, int64_t top_k, float alpha, const void* A, int64_t lda,
+                        tbg_dtype ab_dtype, const void* codes, int64_t ldb, int64_t stride_b, const void* scales,
+                        int64_t ld_s, int64_t stride_s, const uint8_t* zeros, int64_t ld_z, int64_t stride_z, float beta,
+                        void* C, int64_t ldc, tbg_dtype c_dtype, void* stream) {
+  const bool ragged = groups >= 0;
+  tbg_status st = check_sizes(M, N, K);
+  if (st == TBG_OK) st = check_types(ab_dtype, c_dtype);
+  if (st != TBG_OK) return st;
+  if (group != 32 && group != 64 && group != 128)
+    return fail(TBG_ERR_INVALID_VALUE, "group=%lld: 32, 64 or 128", (ll)group);
+  if (K % group != 0) return fail(TBG_ERR_INVALID_VALUE, "K=%lld is not a multiple of group=%lld", (ll)K, (ll)group);
+  if (source && (a_rows < 0 || top_k < 1))
+    return fail(TBG_ERR_INVALID_VALUE, "source needs a_rows >= 0 and top_k >= 1 (got %lld, %lld)", (ll)a_rows, (ll)top_k);
+  if (source && (a_rows > kMaxSize || top_k > kMaxSize))
+    return fail(TBG_ERR_UNSUPPORTED, "a_rows and top_k are limited to 2^30 (%lld, %lld)", (ll)a_rows, (ll)top_k);
+  if (((uintptr_t)source) % 4 != 0) return fail(TBG_ERR_MISALIGNED, "source must be 4-byte aligned");
+  const bool scaled = !(alpha == 1.f && beta == 0.f);
+  if (alpha == 0.f) {  // nothing of A or W is used
+    K = 0;
+    A = codes = scales = zeros = nullptr;
+    lda = ldb = ld_s = ld_z = stride_b = stride_s = stride_z = N > 0 ? round_up(N, 16) : 16;
+  }
+  st = check_ld("lda", lda, K, kMaxLdc);
+  if (st == TBG_OK) st = check_ld("ldb", ldb, K / 2, kMaxSize - 1);
+  if (st == TBG_OK) st = check_ld("ld_s", ld_s, N, kMaxLdc);
+  if (st == TBG_OK && zeros) st = check_ld("ld_z", ld_z, N, kMaxLdc);
+  if (st == TBG_OK) st = check_ld("ldc", ldc, N, kMaxLdc);
+  if (st != TBG_OK) return st;
+  if (off16(codes) || ldb % 16 != 0) return fail(TBG_ERR_MISALIGNED, "codes and their pitch must be multiples of 16 bytes");
+  if (((uintptr_t)A | (uintptr_t)scales) % 2 != 0)
+    return fail(TBG_ERR_MISALIGNED, "A and scales must be aligned to their elements");
+  if (((uintptr_t)C) % out_size(c_dtype) != 0) return fail(TBG_ERR_MISALIGNED, "C must be aligned to its elements");
+  const int64_t parts = K / group;
+  if (ragged && groups > 1 && K > 0 && N > 0) {
+    if (stride_b < (N - 1) * ldb + K / 2 || stride_s < (parts - 1) * ld_s + N ||
+        (zeros && stride_z < (parts - 1) * ld_z + N))
+      return fail(TBG_ERR_INVALID_VALUE, "stride_b=%lld, stride_s=%lld or stride_z=%lld below one matrix", (ll)stride_b,
+                  (ll)stride_s, (ll)stride_z);
+    if (stride_b % 16 != 0) return fail(TBG_ERR_MISALIGNED, "stride_b must be a multiple of 16 bytes");
+  }
+  if (groups == 0 || M == 0 || N == 0) return TBG_OK;
+  if (!C) return fail(TBG_ERR_INVALID_VALUE, "C is NULL");
+  if (K > 0 && (!A || !codes || !scales)) return fail(TBG_ERR_INVALID_VALUE, "A, codes or scales is NULL");
+  if (K > 0 && source && a_rows == 0) return fail(TBG_ERR_INVALID_VALUE, "source has no rows of A to name");
+  int cus = 0;
+  st = check_device(&cus);
+  if (st != TBG_OK) return st;
+  const tbg::TileChoice choice = tbg::choose_w4(ragged ? groups : 0, M, N, cus);
+  st = check_grid(choice);
+  if (st != TBG_OK) return st;
+  tbg::W4Params p;
+  memset(&p, 0, sizeof(p));
+  p.g.A = (const uint8_t*)A;
+  p.g.B = (const uint8_t*)codes;
+  p.g.C = C;
+  p.g.offsets = ragged ? offsets : nullptr;
+  p.g.lda = lda * 2;
+  p.g.ldb = ldb;
+  p.g.stride_b = stride_b;
+  p.g.ldc = ldc;
+  p.g.groups = ragged ? (int)groups : 1;
+  p.g.rows = (int)M;
+  p.g.N = (int)N;
+  p.g.K = (int)K;
+  p.g.alpha = alpha;
+  p.g.beta = beta;
+  p.g.scaled = scaled ? 1 : 0;
+  p.scales = (const uint16_t*)scales;
+  p.zeros = zeros;
+  p.ld_s = ld_s;
+  p.stride_s = stride_s;
+  p.ld_z = ld_z;
+  p.stride_z = stride_z;
+  p.source = source;
+  p.top_k = tbg::make_fast_div((uint32_t)(source ? top_k : 1));
+  p.a_rows = (int)(source ? a_rows : M);
+  p.out16 = c_dtype != TBG_F32;
+  tbg::log_choice("w4 gemm groups=%lld M=%lld N=%lld K=%lld group=%lld in=%s out=%s: %dx%d", (ll)(ragged ? groups : 1), (ll)M,
+                  (ll)N, (ll)K, (ll)group, ab_dtype == TBG_F16 ? "f16" : "bf16", c_dtype == TBG_F32 ? "f32" : "16-bit",
+                  choice.bm, choice.bn);
+  return launch_status("w4 gemm",
+                       tbg::launch_w4_gemm(p, ab_dtype == TBG_F16, (int)group, choice, (hipStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+tbg_status tbg_w4_gemm(int64_t M, int64_t N, int64_t K, int64_t group, float alpha, const void* A, int64_t lda,
+                       tbg_dtype ab_dtype, const void* codes, int64_t ldb, const void* scales, int64_t ld_s,
+                       const uint8_t* zeros, int64_t ld_z, float beta, void* C, int64_t ldc, tbg_dtype c_dtype,
+                       void* stream) {
+  return w4_gemm_impl(-1, M, N, K, group, nullptr, nullptr, 0, 1, alpha, A, lda, ab_dtype, codes, ldb, 0, scales, ld_s, 0,
+                      zeros, ld_z, 0, beta, C, ldc, c_dtype, stream);
+}
+
+tbg_status tbg_w4_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group, const int32_t* offsets,
+                               const int32_t* source, int64_t a_rows, int64_t top_k, float alpha, const void* A,
+                               int64_t lda, tbg_dtype ab_dtype, const void* codes, int64_t ldb, int64_t stride_b,
+                               const void* scales, int64_t ld_s, int64_t stride_s, const uint8_t* zeros, int64_t ld_z,
+                               int64_t stride_z, float beta, void* C, int64_t ldc, tbg_dtype c_dtype, void* stream) {
+  const tbg_status st = check_groups(groups, M, offsets);
+  if (st != TBG_OK) return st;
+  return w4_gemm_impl(groups, M, N, K, group, offsets, source, a_rows, top_k, alpha, A, lda, ab_dtype, codes, ldb, stride_b,
+                      scales, ld_s, stride_s, zeros, ld_z, stride_z, beta, C, ldc, c_dtype, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,264 @@
+// Rows to the groups of their experts and back, and the gradients of the way back.
+//
+//   dispatch      out[place[t,j]] = X[t]
+//   combine       out[t] = sum over j of w[t,j]·Y[place[t,j]]          (fp32, j ascending, rounded once)
+//   combine_grad  dY[place[t,j]] = w[t,j]·dout[t],  dw[t,j] = sum over the columns of Y[place[t,j]]·dout[t]
+//
+// All three move bytes, and all go by token: a token's row is read once for its k rows of the groups
+// (by row of the groups it would be read k times), and the rows of one token are its own, so no two
+// workgroups write the same row and nothing is added across workgroups.  A lane takes 16 bytes of a
+// row; the last unit of a row is moved back to end with the row, so that rows of any length take only
+// whole 16-byte accesses (the bytes that two units share get the same values from both).  Rows shorter
+// than that go element by element.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "expert.hpp"
+#include "ragged.hpp"
+
+namespace tbg {
+
+namespace {
+
+// 16 bytes of a row, which may start at any byte (gfx9 takes unaligned multi-dword accesses).
+struct __attribute__((packed, aligned(1))) Raw16 { uint32_t w[4]; };
+
+// Values of a type: 0 fp32, 1 bf16, 2 fp16.
+template <int DT> struct Elem;
+template <> struct Elem<0> { typedef float type; };
+template <> struct Elem<1> { typedef __bf16 type; };
+template <> struct Elem<2> { typedef _Float16 type; };
+
+// V consecutive values.
+template <int DT, int V>
+struct __attribute__((packed, aligned(sizeof(typename Elem<DT>::type)))) Vec { typename Elem<DT>::type v[V]; };
+
+// The first column of a unit: the last unit of a row ends with the row.
+template <int V>
+__device__ __forceinline__ int64_t unit_column(uint32_t u, int64_t cols) {
+  const int64_t c = (int64_t)u * V;
+  return c + V <= cols ? c : cols - V;
+}
+
+// ---- dispatch ------------------------------------------------------------------------------------
+
+// SHORT 0: units of 16 bytes; else rows below 16 bytes, one element of SHORT bytes a unit.
+template <int SHORT>
+__global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= p.units) return;
+  const uint32_t t = fast_div(i, p.div), u = i - t * p.per_row;
+  constexpr int Bytes = SHORT ? SHORT : 16;
+  struct __attribute__((packed, aligned(1))) Unit { uint8_t b[Bytes]; };
+  const int64_t at = unit_column<Bytes>(u, p.cols);  // cols and columns count bytes here
+  const Unit v = *(const Unit*)(p.in + (int64_t)t * p.ld_in + at);
+  const int32_t* place = p.place + (int64_t)t * p.top_k;
+  for (uint32_t j = 0; j < p.top_k; ++j) {
+    const uint32_t row = (uint32_t)place[j];
+    if (row < p.rows) *(Unit*)(p.out + (int64_t)row * p.ld_out + at) = v;
+  }
+}
+
+// ---- combine -------------------------------------------------------------------------------------
+
+// Y: type of the rows, O: type of the sum, V: values a unit, J: rows in flight.
+template <int Y, int O, int V, int J>
+__global__ void __launch_bounds__(256) combine_kernel(RowsParams p) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= p.units) return;
+  const uint32_t t = fast_div(i, p.div), u = i - t * p.per_row;
+  const int64_t c = unit_column<V>(u, p.cols);
+  const int32_t* place = p.place + (int64_t)t * p.top_k;
+  const float* weights = p.weights ? p.weights + (int64_t)t * p.top_k : nullptr;
+  typedef Vec<Y, V> In;
+  const uint8_t* in = p.in + c * (int64_t)sizeof(typename Elem<Y>::type);
+  float sum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum[v] = 0.f;
+  for (uint32_t j0 = 0; j0 < p.top_k; j0 += J) {
+    uint32_t row[J];
+    float w[J];
+    In y[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      row[j] = j0 + j < p.top_k ? (uint32_t)place[j0 + j] : ~0u;
+      w[j] = weights && j0 + j < p.top_k ? weights[j0 + j] : 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (row[j] < p.rows) y[j] = *(const In*)(in + (int64_t)row[j] * p.ld_in);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (row[j] < p.rows) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum[v] = fmaf(w[j], (float)y[j].v[v], sum[v]);
+      }
+  }
+  Vec<O, V> o;
+#pragma unroll
+  for (int v = 0; v < V; ++v) o.v[v] = (typename Elem<O>::type)sum[v];
+  *(Vec<O, V>*)(p.out + (int64_t)t * p.ld_out + c * (int64_t)sizeof(typename Elem<O>::type)) = o;
+}
+
+// ---- combine_grad --------------------------------------------------------------------------------
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// A workgroup of W waves a token; J of its rows at a time.  Y: type of the rows, D: of dout.
+template <int Y, int D, int V, int J, int W>
+__global__ void __launch_bounds__(64 * W) combine_grad_kernel(RowsParams p) {
+  __shared__ float part[W][J];
+  const uint32_t t = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t* place = p.place + (int64_t)t * p.top_k;
+  typedef typename Elem<Y>::type elem;
+  const uint8_t* dout = p.dout + (int64_t)t * p.ld_dout;
+  for (uint32_t j0 = 0; j0 < p.top_k; j0 += J) {
+    uint32_t row[J];
+    float w[J], dot[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const bool in = j0 + j < p.top_k;
+      row[j] = in ? (uint32_t)place[j0 + j] : ~0u;
+      w[j] = in && p.weights ? p.weights[(int64_t)t * p.top_k + j0 + j] : 1.f;
+      dot[j] = 0.f;
+    }
+    for (uint32_t u = threadIdx.x; u < p.per_row; u += 64 * W) {
+      const int64_t c = unit_column<V>(u, p.cols);
+      const int shared = (int)((int64_t)u * V - c);  // values that the unit before has counted
+      const Vec<D, V> d = *(const Vec<D, V>*)(dout + c * (int64_t)sizeof(typename Elem<D>::type));
+      Vec<Y, V> y[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (row[j] < p.rows) y[j] = *(const Vec<Y, V>*)(p.in + (int64_t)row[j] * p.ld_in + c * (int64_t)sizeof(elem));
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (row[j] >= p.rows) continue;
+        Vec<Y, V> g;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float x = (float)d.v[v];
+          dot[j] = v >= shared ? fmaf((float)y[j].v[v], x, dot[j]) : dot[j];
+          g.v[v] = (elem)(w[j] * x);
+        }
+        *(Vec<Y, V>*)(p.out + (int64_t)row[j] * p.ld_out + c * (int64_t)sizeof(elem)) = g;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float s = wave_sum(dot[j]);
+      if (W > 1 && lane == 0) part[wave][j] = s;
+      if (W == 1 && lane == 0 && j0 + j < p.top_k) p.dweights[(int64_t)t * p.top_k + j0 + j] = s;
+    }
+    if (W > 1) {
+      __syncthreads();
+      if (threadIdx.x < J && j0 + threadIdx.x < p.top_k) {
+        float s = 0.f;
+        for (int k = 0; k < W; ++k) s += part[k][threadIdx.x];
+        p.dweights[(int64_t)t * p.top_k + j0 + threadIdx.x] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Tokens that one launch takes: their units are numbered in 32 bits.
+template <class Launch>
+hipError_t by_tokens(const RowsParams& p, Launch launch) {
+  const int64_t most = ((1ll << 32) - 256) / p.per_row, all = p.tokens;
+  for (int64_t t = 0; t < all; t += most) {
+    const int64_t n = all - t < most ? all - t : most;
+    RowsParams q = p;
+    q.tokens = (uint32_t)n;
+    q.units = (uint32_t)(n * p.per_row);
+    q.place += t * p.top_k;
+    if (q.weights) q.weights += t * p.top_k;
+    launch(q, t, (unsigned)((q.units + 255ull) / 256));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int Y, int O, int V>
+hipError_t combine_units(RowsParams p, hipStream_t s) {
+  p.per_row = (uint32_t)((p.cols + V - 1) / V);
+  p.div = make_fast_div(p.per_row);
+  return by_tokens(p, [&](RowsParams q, int64_t t, unsigned grid) {
+    q.out += t * p.ld_out;
+    if (p.top_k <= 2) hipLaunchKernelGGL((combine_kernel<Y, O, V, 2>), dim3(grid), dim3(256), 0, s, q);
+    else if (p.top_k <= 4) hipLaunchKernelGGL((combine_kernel<Y, O, V, 4>), dim3(grid), dim3(256), 0, s, q);
+    else hipLaunchKernelGGL((combine_kernel<Y, O, V, 8>), dim3(grid), dim3(256), 0, s, q);
+  });
+}
+
+template <int Y, int O>
+hipError_t combine_types(const RowsParams& p, hipStream_t s) {
+  constexpr int V = Y == 0 ? 4 : 8;
+  return p.cols >= V ? combine_units<Y, O, V>(p, s) : combine_units<Y, O, 1>(p, s);
+}
+
+template <int Y, int D, int V, int J>
+hipError_t grad_rows(const RowsParams& p, hipStream_t s) {
+  const int64_t most = (1 << 22) - 1;  // workgroups of 256 threads a launch, counted in 32 bits
+  for (int64_t t = 0; t < p.tokens; t += most) {
+    const int64_t n = p.tokens - t < most ? p.tokens - t : most;
+    RowsParams q = p;
+    q.dout += t * p.ld_dout;
+    q.place += t * p.top_k;
+    if (q.weights) q.weights += t * p.top_k;
+    q.dweights += t * p.top_k;
+    hipLaunchKernelGGL((combine_grad_kernel<Y, D, V, J, 4>), dim3((unsigned)n), dim3(256), 0, s, q);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int Y, int D, int V>
+hipError_t grad_units(RowsParams p, hipStream_t s) {
+  p.per_row = (uint32_t)((p.cols + V - 1) / V);
+  if (p.top_k <= 2) return grad_rows<Y, D, V, 2>(p, s);
+  if (p.top_k <= 4) return grad_rows<Y, D, V, 4>(p, s);
+  return grad_rows<Y, D, V, 8>(p, s);
+}
+
+template <int Y, int D>
+hipError_t grad_types(const RowsParams& p, hipStream_t s) {
+  constexpr int V = Y == 0 ? 4 : 8;
+  return p.cols >= V ? grad_units<Y, D, V>(p, s) : grad_units<Y, D, 1>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_expert_dispatch(RowsParams p, int size, hipStream_t stream) {
+  p.cols *= size;
+  const int unit = p.cols >= 16 ? 16 : size;
+  p.per_row = (uint32_t)((p.cols + unit - 1) / unit);
+  p.div = make_fast_div(p.per_row);
+  return by_tokens(p, [&](RowsParams q, int64_t t, unsigned grid) {
+    q.in += t * p.ld_in;
+    if (unit == 16) hipLaunchKernelGGL((dispatch_kernel<0>), dim3(grid), dim3(256), 0, stream, q);
+    else if (unit == 4) hipLaunchKernelGGL((dispatch_kernel<4>), dim3(grid), dim3(256), 0, stream, q);
+    else if (unit == 2) hipLaunchKernelGGL((dispatch_kernel<2>), dim3(grid), dim3(256), 0, stream, q);
+    else hipLaunchKernelGGL((dispatch_kernel<1>), dim3(grid), dim3(256), 0, stream, q);
+  });
+}
+
+hipError_t launch_expert_combine(RowsParams p, int y, int out, hipStream_t stream) {
+  if (y == 0) return combine_types<0, 0>(p, stream);
+  if (y == 1) return out ? combine_types<1, 1>(p, stream) : combine_types<1, 0>(p, stream);
+  return out ? combine_types<2, 2>(p, stream) : combine_types<2, 0>(p, stream);
+}
+
+hipError_t launch_expert_combine_grad(RowsParams p, int y, int d, hipStream_t stream) {
+  if (y == 0) return grad_types<0, 0>(p, stream);
+  if (y == 1) return d ? grad_types<1, 1>(p, stream) : grad_types<1, 0>(p, stream);
+  return d ? grad_types<2, 2>(p, stream) : grad_types<2, 0>(p, stream);
+}
+
+}  // namespace tbg

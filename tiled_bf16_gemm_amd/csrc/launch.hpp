@@ -168,6 +168,22 @@ hipError_t launch_mx4_gemm(Mx4GemmParams p, const TileChoice& c, int out_bf16, h
 // fp16 (A, B and their pitches as GroupedParams), 2 microscaled 4-bit; out as launch_grouped.
 hipError_t launch_few_rows(Mx4GemmParams p, const TileChoice& c, int fmt, int out, hipStream_t stream);
 
+// Arguments of the products with weights in 4-bit codes (gemm_w4.hpp): g.A activations (rows at lda bytes),
+// g.B codes (N rows at ldb bytes, a matrix of a group stride_b bytes after the last), g.offsets null: one dense
+// product of g.rows rows.  Scales and zeros K/group × N at ld_s (ld_z) elements, matrices at stride_s (stride_z).
+struct W4Params {
+  GroupedParams g;
+  const uint16_t* scales;
+  const uint8_t* zeros;   // null: every zero is 8
+  int64_t ld_s, stride_s, ld_z, stride_z;
+  const int32_t* source;  // null, or row r reads row source[r] / top_k of A's a_rows
+  FastDiv top_k;
+  int a_rows;
+  int out16;              // C has A's type, else fp32
+};
+// in: 0 bf16, 1 fp16; group 32, 64 or 128
+hipError_t launch_w4_gemm(W4Params p, int in, int group, const TileChoice& c, hipStream_t stream);
+
 // fp8 GEMM (gemm_fp8.hpp): p in units of two fp8 values (lda, ldb, K, kchunks as for 16-bit data
 // of half the width); fmt 0 E4M3, 1 E5M2; tiles 256×256, 128×128, 64×64.
 hipError_t launch_fp8(GemmParams p, int bm, int bn, int fmt, int out_bf16, hipStream_t stream);

@@ -178,4 +178,15 @@ inline TileChoice choose_mx4(int64_t groups, int64_t M, int64_t N, int64_t K, in
   return c;
 }
 
+// Rows times weights in 4-bit codes, dense (groups == 0) or ragged.
+inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, int cus) {
+  TileChoice c{};
+  const double active = groups > 0 ? (double)(groups < M ? groups : M) : 1.0, rows = (double)M / active;
+  c.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  c.bn = c.bm == 64 ? 32 : c.bm == 32 ? 64 : narrow_tiles(active, N) >= 2.0 * cus ? 64 : 16;
+  set_row_tiles(c, groups, M, N);
+  c.grid = whole_eighths(c.grid);
+  return c;
+}
+
 }  // namespace tbg

@@ -393,6 +393,203 @@ def mx4_gemm_grouped(A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b
     return out
 
 
+# ---- tokens by expert ------------------------------------------------------------------------------
+
+_ELEMENT_OF = {1: "u8", 2: "u16", 4: "u32"}
+
+
+def _require_ints(t: torch.Tensor, name: str, index: int):
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} is on {t.device}: every operand must be on one CUDA (HIP) device")
+
+
+def _require_place(place: torch.Tensor, weights: Optional[torch.Tensor], index: int):
+    """(tokens, top_k) of place, and the weights that belong to it."""
+    _require_ints(place, "place", index)
+    if place.dim() != 2:
+        raise ValueError("place must be (tokens, top_k)")
+    if weights is not None and (weights.dtype != torch.float32 or not weights.is_contiguous() or
+                                weights.shape != place.shape or weights.get_device() != index):
+        raise ValueError(f"weights must be a contiguous float32 tensor of place's shape {tuple(place.shape)} and device")
+    return place.shape
+
+
+def expert_sort(experts: torch.Tensor, groups: int, workspace: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None):
+    """A router's choices, int32 (tokens, top_k) or (slots,), sorted by expert through tbg_expert_sort.
+    Returns int32 (offsets, source, place): offsets (groups + 1,) of the ragged products, source (slots,)
+    with the slot token·top_k + choice of every row (-1 behind the last group), place of experts' shape
+    with the row of every slot (-1: an expert outside 0..groups-1, a padded or dropped slot)."""
+    index = experts.get_device()
+    _require_ints(experts, "experts", index)
+    slots = experts.numel()
+    with _Launch(index, stream) as handle:
+        offsets = torch.empty(groups + 1, dtype=torch.int32, device=index)
+        source = torch.empty(slots, dtype=torch.int32, device=index)
+        place = torch.empty_like(experts)
+        need = tbg.expert_sort_workspace_query(slots, groups) if slots > 512 else 0
+        ws_ptr, ws_bytes, held = _workspace(need, workspace, experts.device)
+        tbg.expert_sort(slots, groups, experts.data_ptr(), offsets.data_ptr(), source.data_ptr(), place.data_ptr(), ws_ptr,
+                        ws_bytes, handle)
+    return offsets, source, place
+
+
+def expert_dispatch(X: torch.Tensor, place: torch.Tensor, out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out[place[t, j]] = X[t] through tbg_expert_dispatch: the rows of the groups.  X: (tokens, cols) of
+    1-, 2- or 4-byte elements (mx4_quantize's codes and scales among them); place as expert_sort gives it.
+    Rows that no slot holds keep what `out` holds (without `out`, which has a row for every slot:
+    undefined).  The gradient of X is expert_combine(dout, place)."""
+    index = X.get_device()
+    (tokens, cols), st = _require_rows(X, "X", index)
+    placed, top_k = _require_place(place, None, index)
+    size = X.element_size()
+    if placed != tokens:
+        raise ValueError(f"X has {tokens} tokens, place {placed}")
+    if size not in _ELEMENT_OF:
+        raise ValueError(f"X must have elements of 1, 2 or 4 bytes (got {X.dtype})")
+    with _Launch(index, stream) as handle:
+        if out is None:
+            out = torch.empty((tokens * top_k, cols), dtype=X.dtype, device=index)
+        shape, st_o = _require_rows(out, "out", index)
+        if out.dtype != X.dtype or shape[1] != cols:
+            raise ValueError(f"out must be (rows, {cols}) {X.dtype} (got {tuple(shape)} {out.dtype})")
+        tbg.expert_dispatch(tokens, top_k, shape[0], cols, _ELEMENT_OF[size], X.data_ptr(), _pitch((tokens, cols), st),
+                            place.data_ptr(), out.data_ptr(), _pitch(shape, st_o), handle)
+    return out
+
+
+def expert_combine(Y: torch.Tensor, place: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[str] = None, out: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """out[t] = sum over j of weights[t, j]·Y[place[t, j]] through tbg_expert_combine.  Y: (rows, cols) fp32,
+    bf16 or fp16; place as expert_sort gives it (a slot without a row adds nothing); weights: float32 of
+    place's shape, or None for ones.  out_dtype: "f32" or Y's type (default).  Gradients:
+    expert_combine_grad."""
+    index = Y.get_device()
+    (rows, cols), st = _require_rows(Y, "Y", index)
+    tokens, top_k = _require_place(place, weights, index)
+    y_dtype = _X_OF.get(Y.dtype)
+    if y_dtype is None:
+        raise ValueError("Y must be float32, bfloat16 or float16")
+    out_dtype = out_dtype or y_dtype
+    with _Launch(index, stream) as handle:
+        out = _output(out, (tokens, cols), out_dtype, ("f32", y_dtype), index)
+        tbg.expert_combine(tokens, top_k, rows, cols, Y.data_ptr(), _pitch((rows, cols), st), y_dtype, place.data_ptr(),
+                           weights.data_ptr() if weights is not None else 0, out.data_ptr(),
+                           _pitch((tokens, cols), out.stride()), out_dtype, handle)
+    return out
+
+
+def expert_combine_grad(dout: torch.Tensor, Y: torch.Tensor, place: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                        dy: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """(dY, dweights) of expert_combine(Y, place, weights) for the gradient dout, (tokens, cols) of float32 or
+    Y's type, through tbg_expert_combine_grad: dY[place[t, j]] = weights[t, j]·dout[t] in Y's type (rows that no
+    slot holds keep what `dy` holds, without `dy`: undefined), dweights[t, j] = Y[place[t, j]]·dout[t] in
+    float32 (0 for a slot without a row)."""
+    index = Y.get_device()
+    (rows, cols), st = _require_rows(Y, "Y", index)
+    shape_d, st_d = _require_rows(dout, "dout", index)
+    tokens, top_k = _require_place(place, weights, index)
+    y_dtype, d_dtype = _X_OF.get(Y.dtype), _X_OF.get(dout.dtype)
+    if y_dtype is None or d_dtype not in ("f32", y_dtype):
+        raise ValueError("Y must be float32, bfloat16 or float16, dout float32 or Y's type")
+    if tuple(shape_d) != (tokens, cols):
+        raise ValueError(f"dout must be {(tokens, cols)} (got {tuple(shape_d)})")
+    with _Launch(index, stream) as handle:
+        dy = _output(dy, (rows, cols), y_dtype, (y_dtype,), index)
+        dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=index)
+        tbg.expert_combine_grad(tokens, top_k, rows, cols, dout.data_ptr(), _pitch(shape_d, st_d), d_dtype, Y.data_ptr(),
+                                _pitch((rows, cols), st), y_dtype, place.data_ptr(),
+                                weights.data_ptr() if weights is not None else 0, dy.data_ptr(),
+                                _pitch((rows, cols), dy.stride()), dweights.data_ptr(), handle)
+    return dy, dweights
+
+
+# ---- weights in 4-bit codes ------------------------------------------------------------------------
+
+def _require_w4(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor], a_dtype, index: int, dims: int):
+    """A matrix (dims 2) or stack of matrices (3) in 4-bit codes: its shape (…, N, K), the group, and the
+    pitches and strides of codes, scales and zeros."""
+    shape, st = _require_rows(codes, "codes", index, dims)
+    shape_s, st_s = _require_rows(scales, "scales", index, dims)
+    if codes.dtype is not torch.uint8 or scales.dtype is not a_dtype:
+        raise ValueError(f"codes must be uint8 and scales of A's type {a_dtype} (got {codes.dtype}, {scales.dtype})")
+    N, K = shape[-2], 2 * shape[-1]
+    parts = shape_s[-2]
+    if shape_s[-1] != N or shape_s[0] != (shape[0] if dims == 3 else parts):
+        raise ValueError(f"scales {tuple(shape_s)} do not belong to codes {tuple(shape)}")
+    if (parts == 0) != (K == 0) or (parts and (K % parts or K // parts not in (32, 64, 128))):
+        raise ValueError(f"K={K} over {parts} rows of scales: groups must be of 32, 64 or 128")
+    if zeros is None:
+        z, ld_z, stride_z = 0, 0, 0
+    else:
+        shape_z, st_z = _require_rows(zeros, "zeros", index, dims)
+        if zeros.dtype is not torch.uint8 or shape_z != shape_s:
+            raise ValueError(f"zeros must be uint8 of scales' shape {tuple(shape_s)}")
+        z, ld_z, stride_z = zeros.data_ptr(), st_z[-2] if parts > 1 else max(N, 1), st_z[0]
+    return (N, K, K // parts if parts else 32, codes.data_ptr(), st[-2] if N > 1 and K > 0 else max(-(-K // 32), 1) * 16, st[0],
+            scales.data_ptr(), st_s[-2] if parts > 1 else max(N, 1), st_s[0], z, ld_z, stride_z)
+
+
+def w4_gemm(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None,
+            out_dtype: str = "bf16", out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+            alpha: float = 1.0, beta: float = 0.0) -> torch.Tensor:
+    """C = alpha·A·Wᵀ + beta·C for weights in 4-bit codes through tbg_w4_gemm.  A: (M, K) bf16 or fp16; codes:
+    (N, K/2) uint8, the lower nibble first, 16-byte aligned and pitched; scales: (K/group, N) of A's type and
+    zeros: (K/group, N) uint8 or None (every zero is 8), group 32, 64 or 128:
+    W[n, k] = scales[k//group, n]·(code[n, k] - zeros[k//group, n]).  out_dtype: "f32" or A's type; beta != 0
+    needs `out`."""
+    index = A.get_device()
+    (M, Ka), st_a = _require_rows(A, "A", index)
+    ab = _AB_OF.get(A.dtype)
+    if ab not in ("bf16", "f16"):
+        raise ValueError("A must be bfloat16 or float16")
+    N, K, group, c, ldb, _, s, ld_s, _, z, ld_z, _ = _require_w4(codes, scales, zeros, A.dtype, index, 2)
+    if Ka != K:
+        raise ValueError(f"inner sizes differ: {Ka} vs {K}")
+    with _Launch(index, stream) as handle:
+        out = _output(out, (M, N), out_dtype, ("f32", ab), index, beta)
+        tbg.w4_gemm(M, N, K, group, alpha, A.data_ptr(), _pitch((M, K), st_a), ab, c, ldb, s, ld_s, z, ld_z, beta,
+                    out.data_ptr(), _pitch((M, N), out.stride()), out_dtype, handle)
+    return out
+
+
+def w4_gemm_grouped(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                    zeros: Optional[torch.Tensor] = None, source: Optional[torch.Tensor] = None, top_k: int = 1,
+                    out_dtype: str = "bf16", out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None, alpha: float = 1.0, beta: float = 0.0) -> torch.Tensor:
+    """w4_gemm for the rows of every group (offsets as gemm_grouped) with its own W, codes (groups, N, K/2),
+    scales and zeros (groups, K/group, N), through tbg_w4_gemm_grouped.  With `source` (expert_sort's, one slot
+    a row) row r reads A[source[r] // top_k]: the experts' rows of A's tokens without a copy.  Rows of no group
+    keep what `out` holds (without `out`: undefined); beta != 0 needs `out`."""
+    index = A.get_device()
+    (a_rows, Ka), st_a = _require_rows(A, "A", index)
+    ab = _AB_OF.get(A.dtype)
+    if ab not in ("bf16", "f16"):
+        raise ValueError("A must be bfloat16 or float16")
+    groups = _require_offsets(offsets, index)
+    N, K, group, c, ldb, sb, s, ld_s, ss, z, ld_z, sz = _require_w4(codes, scales, zeros, A.dtype, index, 3)
+    if Ka != K:
+        raise ValueError(f"inner sizes differ: {Ka} vs {K}")
+    if codes.shape[0] != groups:
+        raise ValueError(f"codes hold {codes.shape[0]} matrices, offsets {groups} groups")
+    M, src = a_rows, 0
+    if source is not None:
+        _require_ints(source, "source", index)
+        if source.dim() != 1:
+            raise ValueError("source must be (rows,)")
+        M, src = source.shape[0], source.data_ptr()
+    with _Launch(index, stream) as handle:
+        out = _output(out, (M, N), out_dtype, ("f32", ab), index, beta)
+        tbg.w4_gemm_grouped(groups, M, N, K, group, offsets.data_ptr(), src, a_rows, top_k, alpha, A.data_ptr(),
+                            _pitch((a_rows, K), st_a), ab, c, ldb, sb, s, ld_s, ss, z, ld_z, sz, beta, out.data_ptr(),
+                            _pitch((M, N), out.stride()), out_dtype, handle)
+    return out
+
+
 def encode(t: torch.Tensor, dtype: str, dims: Sequence[int], strides_bytes: Sequence[int], box: Sequence[int],
            estr: Sequence[int], swizzle: str = "none", oob: str = "zero", l2: str = "none") -> tbg.TensorDesc:
     """Descriptor for the tensor whose element (0, ..., 0) is t's first element."""
