@@ -629,9 +629,11 @@ tbg_status tbg_expert_combine_grad(int64_t tokens, int64_t top_k, int64_t rows, 
  * elements) and a weight matrix as above; C TBG_F32 or A's type, ldc >= N.
  * Per group the sum of A times whole numbers is held in fp32, multiplied by the scale and added in fp32;
  * nothing else is rounded before C, once, to nearest even.  alpha, beta as tbg_gemm_ex.  Made for few rows
- * (the bytes of W are the cost); any number is taken.
+ * (the bytes of W are the cost); any number is taken.  Codes are read to whole 16 bytes, scales and zeros only
+ * inside the matrix.
  * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.
- * Limits: M, N, K up to 2^30, ldb below 2^30, workgroups as for the ragged products.
+ * Limits: M up to 2^30, ldb below 2^23 (K up to 2^24 - 32), ld_s and ld_z up to 2^28 (N too), workgroups as for the
+ * ragged products.
  * Returns INVALID_VALUE (negative sizes, group, K % group, pitches, null pointers, types), MISALIGNED,
  * UNSUPPORTED (limits), NO_DEVICE / HIP. */
 tbg_status tbg_w4_gemm(int64_t M, int64_t N, int64_t K, int64_t group, float alpha, const void* A, int64_t lda,

@@ -55,10 +55,12 @@ DENSE = [
     (dict(codes=PTR + 8), tbg.ERR_MISALIGNED),
     (dict(ldb=72), tbg.ERR_MISALIGNED),
     (dict(ldb=48), tbg.ERR_INVALID_VALUE),
-    (dict(ldb=1 << 30), tbg.ERR_UNSUPPORTED),
+    (dict(ldb=1 << 23), tbg.ERR_UNSUPPORTED),
     (dict(scales=0), tbg.ERR_INVALID_VALUE),
     (dict(scales=PTR + 1), tbg.ERR_MISALIGNED),
     (dict(ld_s=15), tbg.ERR_INVALID_VALUE),
+    (dict(ld_s=(1 << 28) + 1), tbg.ERR_UNSUPPORTED),
+    (dict(ld_z=(1 << 28) + 1), tbg.ERR_UNSUPPORTED),
     (dict(ld_z=15), tbg.ERR_INVALID_VALUE),
     (dict(lda=127), tbg.ERR_INVALID_VALUE),
     (dict(ldc=15), tbg.ERR_INVALID_VALUE),
@@ -161,7 +163,8 @@ def _bound(a, code, s, z, exact, out):
 
 SHAPES = [(1, 1, 32, 32), (1, 16, 128, 128), (3, 17, 96, 32), (16, 64, 256, 64), (5, 100, 192, 64), (17, 33, 640, 128),
           (33, 257, 544, 32), (64, 48, 1152, 128), (65, 130, 2048, 64), (130, 20, 4096, 128), (2, 5000, 160, 32),
-          (20, 9000, 128, 128), (40, 9001, 64, 64), (7, 15, 8192, 32)]
+          (20, 9000, 128, 128), (40, 9001, 64, 64), (7, 15, 8192, 32), (40, 14400, 160, 32), (200, 6200, 192, 64),
+          (100, 12300, 384, 128)]
 
 
 @gpu
@@ -226,33 +229,49 @@ def test_order_of_the_codes():
 
 
 @gpu
-def test_infinities_and_huge_values():
-    """Rows that hold an infinity, a NaN or values near the end of bf16's range come out as the definition's sum."""
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N", [(5, 24700), (30, 24700), (60, 24700), (9, 400), (9, 7000), (9, 12400)])
+def test_every_number_of_blocks(M, N, dtype):
+    """Each kernel over sums of less than one block of 128 up to nine, whole or not."""
+    ops = _ops()
+    for K, G in ((32, 32), (96, 32), (128, 128), (160, 32), (192, 64), (256, 128), (352, 32), (384, 64), (512, 128), (640, 64),
+                 (672, 32), (768, 128), (1088, 64), (1152, 32)):
+        print(f"w4 {M}x{N}x{K} group {G} {dtype}", flush=True)
+        code, s, z = _operands(_gen(K), (), N, K, G, dtype, K % 64 == 0, True)
+        a = torch.randint(-4, 5, (M, K), device="cuda", generator=_gen(K + 1)).to(TORCH[dtype])
+        want = (a.double() @ _weights(code, s, z).t().contiguous()).float()
+        assert torch.equal(ops.w4_gemm(a, _pack(code), s, z, out_dtype="f32"), want)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(40, 70, 512), (40, 24700, 256), (30, 24700, 160), (16, 24700, 96), (16, 12400, 160)])
+def test_infinities_and_huge_values(M, N, K):
+    """Rows that hold an infinity, a NaN or values near the end of bf16's range come out as the definition's sum, and
+    the others are not touched by them."""
     ops = _ops()
     g = _gen(4)
-    N, K, G = 70, 512, 128
+    G, inf, big = 32, float("inf"), 2.0 ** 127
     code, s, z = _operands(g, (), N, K, G, "bf16", True, True)
-    big = 2.0 ** 127
-    for dtype, inf in (("bf16", float("inf")), ("f16", float("inf"))):
+    for dtype in ("bf16", "f16"):
         sc = s.to(TORCH[dtype])
-        a = torch.randint(-4, 5, (40, K), device="cuda", generator=g).to(TORCH[dtype])
-        a[3, 17], a[9, 200], a[11, 5] = inf, -inf, float("nan")
+        a = torch.randint(-4, 5, (M, K), device="cuda", generator=g).to(TORCH[dtype])
+        a[3, 17], a[9, 70], a[11, 5] = inf, -inf, float("nan")
         if dtype == "bf16":
-            a[20, 300], a[20, 301] = big, -big  # c·a passes fp32's range, (c - z)·a or the sum need not
+            a[14, 40], a[14, 41] = big, -big  # c·a passes fp32's range, (c - z)·a or the sum need not
         w = _weights(code, sc, z)
-        exact = a.double() @ w.t().contiguous()
+        rest = [r for r in range(M) if r not in (3, 9, 11, 14)]
+        exact = a[rest].double() @ w.t().contiguous()
         got = ops.w4_gemm(a, _pack(code), sc, z, out_dtype="f32")
         # rows of infinities: inf·0 is NaN, the others infinite with the weight's sign
-        for r, k, sign in ((3, 17, 1.0), (9, 200, -1.0)):
+        for r, k, sign in ((3, 17, 1.0), (9, 70, -1.0)):
             want = torch.where(w[:, k] == 0, float("nan"), sign * w[:, k].sign() * inf)
             assert torch.equal(torch.nan_to_num(got[r].double(), nan=7.0), torch.nan_to_num(want, nan=7.0))
         assert bool(torch.isnan(got[11]).all())
-        rest = [r for r in range(40) if r not in (3, 9, 11, 20)]
-        assert torch.equal(got[rest].double(), exact[rest])
+        assert torch.equal(got[rest].double(), exact)
         if dtype == "bf16":
             cz = code.double() - z.double().t().repeat_interleave(G, -1)
-            fits = (cz[:, 300].abs() <= 1) & (cz[:, 301].abs() <= 1) & (cz[:, 300] == cz[:, 301])
-            assert bool(torch.isfinite(got[20][fits]).all())
+            fits = (cz[:, 40].abs() <= 1) & (cz[:, 41].abs() <= 1)
+            assert bool(torch.isfinite(got[14][fits & (cz[:, 40] == cz[:, 41])]).all())
 
 
 @gpu
@@ -320,7 +339,8 @@ def test_no_sum():
 
 SPLITS = [([1], 16, 128, 128), ([0, 3, 0, 1, 5], 40, 192, 64), ([2, 1, 1, 0, 4, 1, 1, 2], 2048, 256, 128),
           ([17, 0, 31, 16], 100, 320, 32), ([64, 65, 1, 0, 200], 130, 256, 64), ([0, 0, 0], 16, 64, 32),
-          ([3] * 100, 33, 96, 32), ([1] * 70, 700, 128, 64)]
+          ([3] * 100, 33, 96, 32), ([1] * 70, 700, 128, 64),
+          ([40, 1, 90, 33, 0, 70, 64, 22], 2900, 160, 32), ([20, 1, 33, 0, 32, 17, 16, 40] * 2, 2050, 640, 64)]
 
 
 @gpu

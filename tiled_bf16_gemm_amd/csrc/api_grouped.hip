@@ -17,6 +17,7 @@ namespace {
 
 constexpr int64_t kMaxLd = (1ll << 22) - 1;     // elements of a 16-bit operand
 constexpr int64_t kMaxPitch4 = (1ll << 23) - 16;  // bytes of a row of codes or scales
+constexpr int64_t kMaxPitchScales = 1ll << 28;  // elements of a row of scales or zeros
 constexpr int64_t kMaxSize = 1ll << 30;
 constexpr int64_t kMaxLdc = 1ll << 40;
 constexpr int64_t kGroupLimit = 4096;
@@ -494,9 +495,9 @@ tbg_status w4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t
     lda = ldb = ld_s = ld_z = stride_b = stride_s = stride_z = N > 0 ? round_up(N, 16) : 16;
   }
   st = check_ld("lda", lda, K, kMaxLdc);
-  if (st == TBG_OK) st = check_ld("ldb", ldb, K / 2, kMaxSize - 1);
-  if (st == TBG_OK) st = check_ld("ld_s", ld_s, N, kMaxLdc);
-  if (st == TBG_OK && zeros) st = check_ld("ld_z", ld_z, N, kMaxLdc);
+  if (st == TBG_OK) st = check_ld("ldb", ldb, K / 2, kMaxPitch4);
+  if (st == TBG_OK) st = check_ld("ld_s", ld_s, N, kMaxPitchScales);
+  if (st == TBG_OK && zeros) st = check_ld("ld_z", ld_z, N, kMaxPitchScales);
   if (st == TBG_OK) st = check_ld("ldc", ldc, N, kMaxLdc);
   if (st != TBG_OK) return st;
   if (off16(codes) || ldb % 16 != 0) return fail(TBG_ERR_MISALIGNED, "codes and their pitch must be multiples of 16 bytes");
@@ -535,6 +536,9 @@ tbg_status w4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t
   p.g.rows = (int)M;
   p.g.N = (int)N;
   p.g.K = (int)K;
+  p.g.tiles_m = (int)choice.tiles_m;
+  p.g.tiles_n = (int)choice.tiles_n;
+  p.g.group_m = 8;
   p.g.alpha = alpha;
   p.g.beta = beta;
   p.g.scaled = scaled ? 1 : 0;
@@ -548,11 +552,12 @@ tbg_status w4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t
   p.top_k = tbg::make_fast_div((uint32_t)(source ? top_k : 1));
   p.a_rows = (int)(source ? a_rows : M);
   p.out16 = c_dtype != TBG_F32;
-  tbg::log_choice("w4 gemm groups=%lld M=%lld N=%lld K=%lld group=%lld in=%s out=%s: %dx%d", (ll)(ragged ? groups : 1), (ll)M,
-                  (ll)N, (ll)K, (ll)group, ab_dtype == TBG_F16 ? "f16" : "bf16", c_dtype == TBG_F32 ? "f32" : "16-bit",
-                  choice.bm, choice.bn);
-  return launch_status("w4 gemm",
-                       tbg::launch_w4_gemm(p, ab_dtype == TBG_F16, (int)group, choice, (hipStream_t)stream));
+  tbg::log_choice("w4 gemm groups=%lld M=%lld N=%lld K=%lld group=%lld in=%s out=%s: %s %dx%d",
+                  (ll)(ragged ? groups : 1), (ll)M, (ll)N, (ll)K, (ll)group, ab_dtype == TBG_F16 ? "f16" : "bf16",
+                  c_dtype == TBG_F32 ? "f32" : "16-bit", choice.few ? "rows" : "panel", choice.bm, choice.bn);
+  const auto launch = ab_dtype == TBG_F16 ? (zeros ? tbg::launch_w4_f16_zeros : tbg::launch_w4_f16)
+                                          : (zeros ? tbg::launch_w4_bf16_zeros : tbg::launch_w4_bf16);
+  return launch_status("w4 gemm", launch(p, (int)group, choice, (hipStream_t)stream));
 }
 
 }  // namespace

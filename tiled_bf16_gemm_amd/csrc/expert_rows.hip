@@ -42,6 +42,11 @@ __device__ __forceinline__ int64_t unit_column(uint32_t u, int64_t cols) {
 
 // ---- dispatch ------------------------------------------------------------------------------------
 
+template <int SHORT> struct Unit { typedef Raw16 type; };
+template <> struct Unit<1> { typedef uint8_t type; };
+template <> struct Unit<2> { typedef uint16_t type; };
+template <> struct Unit<4> { typedef uint32_t type; };
+
 // SHORT 0: units of 16 bytes; else rows below 16 bytes, one element of SHORT bytes a unit.
 template <int SHORT>
 __global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
@@ -49,13 +54,13 @@ __global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
   if (i >= p.units) return;
   const uint32_t t = fast_div(i, p.div), u = i - t * p.per_row;
   constexpr int Bytes = SHORT ? SHORT : 16;
-  struct __attribute__((packed, aligned(1))) Unit { uint8_t b[Bytes]; };
+  typedef typename Unit<SHORT>::type T;
   const int64_t at = unit_column<Bytes>(u, p.cols);  // cols and columns count bytes here
-  const Unit v = *(const Unit*)(p.in + (int64_t)t * p.ld_in + at);
+  const T v = *(const T*)(p.in + (int64_t)t * p.ld_in + at);
   const int32_t* place = p.place + (int64_t)t * p.top_k;
   for (uint32_t j = 0; j < p.top_k; ++j) {
     const uint32_t row = (uint32_t)place[j];
-    if (row < p.rows) *(Unit*)(p.out + (int64_t)row * p.ld_out + at) = v;
+    if (row < p.rows) *(T*)(p.out + (int64_t)row * p.ld_out + at) = v;
   }
 }
 

@@ -23,9 +23,10 @@
 // 32j + 8(l/16) .. +7.  A's fragment is the 16 bytes at that k, its values in the order in which decoding
 // leaves the codes.
 //
-// A workgroup owns 16·FM rows and 16·FN columns; its waves split K by blocks of 128 and their sums meet in
-// LDS, added in wave order: one launch, no workspace, the same bits every time.  Rows and columns past the
-// end repeat the last one and are not stored.
+// Two kernels, both one launch without a workspace, with the same bits every time: for few tiles the waves of
+// a workgroup split K and their sums meet in LDS, added in wave order; for many they split N and share A's
+// blocks in LDS.  Rows and columns past the end repeat the last one and are not stored.  choose_w4
+// (tile_choice.hpp) has both sides' figures.
 #pragma once
 #include "gemm_common.hpp"
 #include "ragged.hpp"
@@ -100,54 +101,84 @@ __device__ __forceinline__ void turn_quarters(u32x4_t& b) {
   b = u32x4_t{r0, r1, r2, r3};
 }
 
-// What a wave holds of a block of 128 codes: FM fragments of rows, FN of columns.
-template <int G, int FM, int FN>
-struct W4Block {
+// What a wave holds of the weights of a block of 128 codes, FN fragments of columns.
+template <int G, int FN>
+struct W4Weights {
   static constexpr int Groups = kW4Block / G;
-  u32x4_t a[FM][4];
   u32x4_t b[FN];
   uint16_t s[Groups][FN];
   uint8_t z[Groups][FN];
 };
 
-// Where a lane reads: its rows of A (at its quarter's 16 bytes), its columns' codes, scales and zeros.
-template <int FM, int FN>
-struct W4Lane {
-  const uint8_t* a[FM];
-  const uint8_t* b[FN];
-  const uint16_t* s;
-  const uint8_t* z;  // null: every zero is 8
-  int64_t ld_s, ld_z;
-  int col[FN];
+// Where a lane reads its columns' codes, scales and zeros: from the tile's bases, the same for every lane.
+template <int FN>
+struct W4Columns {
+  const uint8_t* b;    // the first column's codes
+  const uint8_t* s;    // its scales
+  const uint8_t* z;    // its zeros
+  int64_t ld_s, ld_z;  // bytes
+  uint32_t at_b[FN], at_s[FN], at_z[FN];
 };
 
-// Block c; ALL: it is whole, else it has `steps` steps of 32 (what is past them is left unread).
-template <bool ALL, int G, int FM, int FN>
-__device__ __forceinline__ void load_block(W4Block<G, FM, FN>& k, const W4Lane<FM, FN>& l, int c, int steps, int quarter) {
+// Columns n0, n0 + 1, ... of W_group, the lane's at n0 + 16·n + lane%16.
+template <int FN>
+__device__ __forceinline__ W4Columns<FN> w4_columns(const W4Params& p, int group, int n0, int lane) {
+  W4Columns<FN> l;
+  l.b = p.g.B + (int64_t)group * p.g.stride_b + (int64_t)n0 * p.g.ldb;
+  l.s = (const uint8_t*)(p.scales + (int64_t)group * p.stride_s + n0);
+  l.z = p.zeros ? p.zeros + (int64_t)group * p.stride_z + n0 : nullptr;
+  l.ld_s = 2 * p.ld_s;
+  l.ld_z = p.ld_z;
 #pragma unroll
   for (int n = 0; n < FN; ++n) {
-    k.b[n] = u32x4_t{0, 0, 0, 0};
-    if (ALL || quarter < steps) k.b[n] = *(const u32x4_t*)(l.b[n] + (int64_t)c * 64);
+    l.at_z[n] = (uint32_t)max(min(16 * n + (lane & 15), p.g.N - 1 - n0), 0);
+    l.at_s[n] = 2 * l.at_z[n];
+    l.at_b[n] = l.at_z[n] * (uint32_t)p.g.ldb;
   }
+  return l;
+}
+
+// Block c, of which `steps` steps of 32 exist (ALL: four).  What is past them repeats what exists; the products
+// leave it out.  Nothing is computed with what is loaded here, which would wait for it.
+template <bool ALL, bool ZEROS, int G, int FN>
+__device__ __forceinline__ void load_weights(W4Weights<G, FN>& k, const W4Columns<FN>& l, int c, int steps, int quarter) {
+  const uint8_t* b = l.b + (int64_t)c * 64;
+  const uint32_t q = ALL || quarter < steps ? quarter * 16 : 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int n = 0; n < FN; ++n) k.b[n] = *(const u32x4_t*)(b + (l.at_b[n] + q));
 #pragma unroll
-    for (int m = 0; m < FM; ++m) {
-      if (ALL || j < steps) {
-        const W4Raw16 r = *(const W4Raw16*)(l.a[m] + (int64_t)c * 256 + j * 64);
-        k.a[m][j] = u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]};
-      }
-    }
-#pragma unroll
-  for (int g = 0; g < W4Block<G, FM, FN>::Groups; ++g) {
-    if (!ALL && g * (G / 32) >= steps) break;
-    const int64_t row = (int64_t)c * W4Block<G, FM, FN>::Groups + g;
+  for (int g = 0; g < W4Weights<G, FN>::Groups; ++g) {
+    const int64_t row = (int64_t)c * W4Weights<G, FN>::Groups + (ALL || g * (G / 32) < steps ? g : 0);
+    const uint8_t *s = l.s + row * l.ld_s, *z = l.z + row * l.ld_z;
 #pragma unroll
     for (int n = 0; n < FN; ++n) {
-      k.s[g][n] = l.s[row * l.ld_s + l.col[n]];
-      k.z[g][n] = l.z ? l.z[row * l.ld_z + l.col[n]] : (uint8_t)8;
+      k.s[g][n] = *(const uint16_t*)(s + l.at_s[n]);
+      if (ZEROS) k.z[g][n] = z[l.at_z[n]];
     }
   }
+}
+
+// The activations of a block in registers, one fragment of 16 rows; row: the lane's row at its quarter's bytes.
+struct W4Rows {
+  u32x4_t a[4];
+};
+
+template <bool ALL>
+__device__ __forceinline__ void load_rows(W4Rows& k, const uint8_t* row, int c, int steps) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (!ALL) k.a[j] = u32x4_t{0, 0, 0, 0};
+    if (ALL || j < steps) {
+      const W4Raw16 r = *(const W4Raw16*)(row + (int64_t)c * 256 + j * 64);
+      k.a[j] = u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]};
+    }
+  }
+}
+
+// The row of A that row r of the groups reads.
+__device__ __forceinline__ int64_t w4_row(const W4Params& p, int r) {
+  if (!p.source || p.g.K == 0) return r;
+  return min((int)fast_div((uint32_t)max(p.source[r], 0), p.top_k), p.a_rows - 1);
 }
 
 template <int IN>
@@ -156,157 +187,394 @@ __device__ __forceinline__ float scale_value(uint16_t s) {
   return __uint_as_float((uint32_t)s << 16);
 }
 
-template <bool ALL, int IN, bool EXACT, int G, int FM, int FN>
-__device__ __forceinline__ void block_products(f32x4_t (&acc)[FM][FN], W4Block<G, FM, FN>& k, int steps) {
+// A group's scale and zero for a lane's column.
+struct W4Scale {
+  float s, z;
+};
+
+template <int IN, bool ZEROS, int G, int FN>
+__device__ __forceinline__ auto scales_of(const W4Weights<G, FN>& k) {
+  return [&k](int g, int n) __attribute__((always_inline)) {
+    return W4Scale{scale_value<IN>(k.s[g][n]), ZEROS ? (float)k.z[g][n] : 8.f};
+  };
+}
+
+// Groups of a block from step `steps` on do not exist: their scales count as zero (and A's values as zeros).
+template <int G, int FN>
+__device__ __forceinline__ void end_weights(W4Weights<G, FN>& k, int steps) {
+#pragma unroll
+  for (int g = 0; g < W4Weights<G, FN>::Groups; ++g)
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+      if (g * (G / 32) >= steps) k.s[g][n] = 0;
+}
+
+// acc += the products of a block whose codes are b.  fragment(m, j) gives A's fragment m of step j, in decode's
+// order, scale(g, n) the scale and zero of group g of the block.
+template <int IN, bool EXACT, int G, int FM, int FN, class Fragment, class Scale>
+__device__ __forceinline__ void block_products(f32x4_t (&acc)[FM][FN], u32x4_t (&b)[FN], Fragment fragment, Scale scale) {
   constexpr bool Sums = IN == 0 && !EXACT;  // z is taken off after the group
   const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-  for (int n = 0; n < FN; ++n) turn_quarters(k.b[n]);
+  for (int n = 0; n < FN; ++n) turn_quarters(b[n]);
+  f32x4_t sum[FM][FN], of_a[FM];
+  W4Scale sz[FN];
+  bf16x8_t a[2][FM];
 #pragma unroll
-  for (int g = 0; g < W4Block<G, FM, FN>::Groups; ++g) {
-    if (!ALL && g * (G / 32) >= steps) break;
-    f32x4_t sum[FM][FN], of_a[FM];
-    float z[FN];
+  for (int m = 0; m < FM; ++m) a[0][m] = fragment(m, 0);
 #pragma unroll
-    for (int m = 0; m < FM; ++m) {
-      of_a[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int n = 0; n < FN; ++n) sum[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-#pragma unroll
-    for (int n = 0; n < FN; ++n) z[n] = (float)k.z[g][n];
-#pragma unroll
-    for (int i = 0; i < G / 32; ++i) {
-      const int j = g * (G / 32) + i;
-      bf16x8_t a[FM];
+  for (int j = 0; j < 4; ++j) {
+    constexpr int Steps = G / 32;
+    if (j % Steps == 0) {
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
-        a[m] = order_a<IN>(k.a[m][j]);
-        if (Sums) mfma16<false, IN>(of_a[m], a[m], __builtin_bit_cast(bf16x8_t, ones));
+        of_a[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < FN; ++n) sum[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
 #pragma unroll
-      for (int n = 0; n < FN; ++n) {
-        const bf16x8_t b = decode<IN, EXACT>(k.b[n][j], z[n]);
+      for (int n = 0; n < FN; ++n) sz[n] = scale(j / Steps, n);
+    }
+    if (j < 3) {
 #pragma unroll
-        for (int m = 0; m < FM; ++m) mfma16<false, IN>(sum[m][n], a[m], b);
-      }
+      for (int m = 0; m < FM; ++m) a[(j + 1) & 1][m] = fragment(m, j + 1);
+    }
+    if (Sums) {
+#pragma unroll
+      for (int m = 0; m < FM; ++m) mfma16<false, IN>(of_a[m], a[j & 1][m], __builtin_bit_cast(bf16x8_t, ones));
     }
 #pragma unroll
     for (int n = 0; n < FN; ++n) {
-      const float s = scale_value<IN>(k.s[g][n]);
+      const bf16x8_t v = decode<IN, EXACT>(b[n][j], sz[n].z);
 #pragma unroll
-      for (int m = 0; m < FM; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = Sums ? fmaf(-z[n], of_a[m][i], sum[m][n][i]) : sum[m][n][i];
-          acc[m][n][i] = fmaf(s, x, acc[m][n][i]);
-        }
+      for (int m = 0; m < FM; ++m) mfma16<false, IN>(sum[m][n], a[j & 1][m], v);
     }
+    if (j % Steps == Steps - 1) {
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = Sums ? fmaf(-sz[n].z, of_a[m][i], sum[m][n][i]) : sum[m][n][i];
+            acc[m][n][i] = fmaf(sz[n].s, x, acc[m][n][i]);
+          }
+      // The sums are used up here: moved into a later block of the code they would stay in registers until there.
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int m = 0; m < FM; ++m) asm volatile("" : "+v"(acc[m][n]));
+    }
+    // Steps stay in this order: decoded further ahead of their products they would take the registers of another
+    // wave, which hides one's decoding under the other's products.
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// The wave's share of the K loop: blocks wave, wave + W, ..., one ahead of the products.
-template <int IN, bool EXACT, int G, int FM, int FN, int W>
-__device__ __forceinline__ void w4_sums(f32x4_t (&acc)[FM][FN], const W4Lane<FM, FN>& l, int K, int wave, int quarter) {
-  const int whole = K / kW4Block, left = K % kW4Block / 32;
+template <int FM, int FN>
+__device__ __forceinline__ void clear_sums(f32x4_t (&acc)[FM][FN]) {
 #pragma unroll
   for (int m = 0; m < FM; ++m)
 #pragma unroll
     for (int n = 0; n < FN; ++n) acc[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  W4Block<G, FM, FN> k0, k1;
-  int c = wave;
-  if (c < whole) load_block<true>(k0, l, c, 4, quarter);
-  for (; c < whole; c += 2 * W) {
-    if (c + W < whole) load_block<true>(k1, l, c + W, 4, quarter);
-    block_products<true, IN, EXACT>(acc, k0, 4);
-    if (c + W >= whole) break;
-    if (c + 2 * W < whole) load_block<true>(k0, l, c + 2 * W, 4, quarter);
-    block_products<true, IN, EXACT>(acc, k1, 4);
+}
+
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.4028235e38f; }
+
+// The tile of this workgroup; false when there is none (the grid is an upper bound).
+template <int BM>
+__device__ __forceinline__ bool w4_tile(const GroupedParams& g, RaggedTile& t) {
+  if (g.offsets) return ragged_tile<BM>(g, g.group_m, blockIdx.x, t);
+  int first, count, tm;
+  xcd_share(g.tiles_m * g.tiles_n, blockIdx.x, first, count);
+  if ((int)(blockIdx.x >> 3) >= count) return false;
+  band_tile(first + (blockIdx.x >> 3), g.tiles_m, g.tiles_n, g.group_m, tm, t.tn);
+  t.group = 0;
+  t.row0 = tm * BM;
+  t.rows = g.rows - t.row0;
+  return true;
+}
+
+// C[row][n] from the sum x.
+template <int IN>
+__device__ __forceinline__ void w4_store(const W4Params& p, int64_t row, int n, float x) {
+  const GroupedParams& g = p.g;
+  typedef typename Half4<IN == 1 ? 2 : 1>::elem half;
+  const int64_t at = row * g.ldc + n;
+  if (g.scaled) {
+    x *= g.alpha;
+    if (g.beta != 0.f) x = fmaf(g.beta, p.out16 ? (float)((const half*)g.C)[at] : ((const float*)g.C)[at], x);
   }
-  if (left > 0 && wave == whole % W) {
-    load_block<false>(k0, l, whole, left, quarter);
-    block_products<false, IN, EXACT>(acc, k0, left);
+  if (p.out16) ((half*)g.C)[at] = (half)x;
+  else ((float*)g.C)[at] = x;
+}
+
+// The tile again, from c - z itself, for a result that is not finite: a wave takes one fragment of 16 rows and 16
+// columns after another over the whole of K and stores it.  Rarely taken, so it is kept small.
+template <int IN, bool ZEROS, int G>
+__device__ __forceinline__ void w4_exact_fragment(const W4Params& p, const RaggedTile& t, int r0, int n0) {
+  const int lane = threadIdx.x & 63, quarter = lane >> 4;
+  const GroupedParams& g = p.g;
+  const uint8_t* const row = g.A + w4_row(p, t.row0 + min(r0 + (lane & 15), t.rows - 1)) * g.lda + quarter * 16;
+  const W4Columns<1> l = w4_columns<1>(p, t.group, n0, lane);
+  f32x4_t acc[1][1];
+  clear_sums(acc);
+  const int whole = g.K / kW4Block, left = g.K % kW4Block / 32;
+#pragma unroll 1
+  for (int c = 0; c < whole + (left > 0); ++c) {
+    const int steps = c < whole ? 4 : left;
+    W4Weights<G, 1> k;
+    W4Rows x;
+    load_weights<false, ZEROS>(k, l, c, steps, quarter);
+    load_rows<false>(x, row, c, steps);
+    end_weights(k, steps);
+    block_products<IN, true, G>(acc, k.b, [&](int, int j) __attribute__((always_inline)) {
+      return order_a<IN>(x.a[j]);
+    }, scales_of<IN, ZEROS>(k));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * quarter + i, n = n0 + (lane & 15);
+    if (r < t.rows && n < g.N) w4_store<IN>(p, t.row0 + r, n, acc[0][0][i]);
   }
 }
 
-template <int IN, int G, int FM, int FN, int W>
-__global__ void __launch_bounds__(64 * W) gemm_w4_kernel(W4Params p) {
-  __shared__ f32x4_t part[W][FM * FN][64];
+// ---- the waves split K ---------------------------------------------------------------------------
+
+constexpr int kW4Waves = 4;
+
+// For few tiles: a workgroup owns 16 rows and 16·FN columns, and its waves split K; everything goes straight from
+// memory to registers, a block ahead of the products.
+template <int IN, bool ZEROS, int G, int FN>
+__global__ void __launch_bounds__(64 * kW4Waves, 2) gemm_w4_kernel(W4Params p) {
+  constexpr int W = kW4Waves;
+  __shared__ f32x4_t part[W][FN][64];
   const GroupedParams& g = p.g;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), quarter = lane >> 4;
   RaggedTile t;
-  if (g.offsets) {
-    if (!ragged_tile<16 * FM>(g, g.group_m, blockIdx.x, t)) return;
-  } else {
-    int first, count, tm;
-    xcd_share(g.tiles_m * g.tiles_n, blockIdx.x, first, count);
-    if ((int)(blockIdx.x >> 3) >= count) return;
-    band_tile(first + (blockIdx.x >> 3), g.tiles_m, g.tiles_n, g.group_m, tm, t.tn);
-    t.group = 0;
-    t.row0 = tm * 16 * FM;
-    t.rows = g.rows - t.row0;
-  }
+  if (!w4_tile<16>(g, t)) return;
   const int n0 = t.tn * 16 * FN;
-  W4Lane<FM, FN> l;
-  l.s = p.scales + (int64_t)t.group * p.stride_s;
-  l.z = p.zeros ? p.zeros + (int64_t)t.group * p.stride_z : nullptr;
-  l.ld_s = p.ld_s;
-  l.ld_z = p.ld_z;
-#pragma unroll
-  for (int m = 0; m < FM; ++m) {
-    int64_t row = t.row0 + min(16 * m + (lane & 15), t.rows - 1);
-    if (p.source && g.K > 0) {
-      const int slot = max(p.source[row], 0);
-      row = min((int)fast_div((uint32_t)slot, p.top_k), p.a_rows - 1);
+  const W4Columns<FN> l = w4_columns<FN>(p, t.group, n0, lane);
+  const uint8_t* const row = g.A + w4_row(p, t.row0 + min(lane & 15, t.rows - 1)) * g.lda + quarter * 16;
+  // The wave's share of K: consecutive blocks (a cache line of codes holds two).
+  const int whole = g.K / kW4Block, left = g.K % kW4Block / 32;
+  const int first = (int)((uint32_t)whole * wave / W), end = (int)((uint32_t)whole * (wave + 1) / W);
+  f32x4_t acc[1][FN];
+  clear_sums(acc);
+  W4Weights<G, FN> k0, k1;
+  W4Rows x0, x1;
+  auto load = [&](W4Weights<G, FN>& k, W4Rows& x, int c) __attribute__((always_inline)) {
+    load_weights<true, ZEROS>(k, l, c, 4, quarter);
+    load_rows<true>(x, row, c, 4);
+  };
+  auto products = [&](W4Weights<G, FN>& k, const W4Rows& x) __attribute__((always_inline)) {
+    block_products<IN, false, G>(acc, k.b, [&](int, int j) __attribute__((always_inline)) {
+      return order_a<IN>(x.a[j]);
+    }, scales_of<IN, ZEROS>(k));
+  };
+  if (first < end) {
+    // Every load of the loop is issued on every path (past the end the last block again): the waits before the
+    // products can then count the loads behind them instead of draining all of them.
+    load(k0, x0, first);
+    int c = first;
+    for (; c + 2 <= end; c += 2) {
+      load(k1, x1, c + 1);
+      products(k0, x0);
+      load(k0, x0, min(c + 2, end - 1));
+      products(k1, x1);
     }
-    l.a[m] = g.A + row * g.lda + quarter * 16;
+    if (c < end) products(k0, x0);
+  }
+  if (left > 0 && wave == W - 1) {
+    load_weights<false, ZEROS>(k0, l, whole, left, quarter);
+    load_rows<false>(x0, row, whole, left);
+    end_weights(k0, left);
+    products(k0, x0);
   }
 #pragma unroll
-  for (int n = 0; n < FN; ++n) {
-    l.col[n] = min(n0 + 16 * n + (lane & 15), g.N - 1);
-    l.b[n] = g.B + (int64_t)t.group * g.stride_b + (int64_t)l.col[n] * g.ldb + quarter * 16;
+  for (int n = 0; n < FN; ++n) part[wave][n][lane] = acc[0][n];
+  __syncthreads();
+  // Thread threadIdx.x takes elements threadIdx.x + 256·i of the tile, a row's columns side by side.
+  float x[FN];
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < FN; ++i) {
+    const int e = threadIdx.x + 64 * W * i, r = e / (16 * FN), n = e % (16 * FN);
+    const int at = ((n >> 4) * 64 + (r >> 2) * 16 + (n & 15)) * 4 + (r & 3);
+    x[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) x[i] += ((const float*)part[w])[at];
+    finite = finite && is_finite(x[i]);
   }
-  // Thread threadIdx.x + 64·W·i of the tile's elements, a row's columns side by side.
-  constexpr int Each = 4 * FM * FN / W;
-  float x[Each];
-  auto compute = [&](auto exact) __attribute__((always_inline)) {
-    f32x4_t acc[FM][FN];
-    w4_sums<IN, decltype(exact)::value, G, FM, FN, W>(acc, l, g.K, wave, quarter);
+  if constexpr (IN == 0) {
+    if (__syncthreads_or(!finite)) {
+#pragma unroll 1
+      for (int n = wave; n < FN; n += W)
+        if (n0 + 16 * n < g.N) w4_exact_fragment<IN, ZEROS, G>(p, t, 0, n0 + 16 * n);
+      return;
+    }
+  }
 #pragma unroll
-    for (int m = 0; m < FM; ++m)
+  for (int i = 0; i < FN; ++i) {
+    const int e = threadIdx.x + 64 * W * i, r = e / (16 * FN), n = n0 + e % (16 * FN);
+    if (r < t.rows && n < g.N) w4_store<IN>(p, t.row0 + r, n, x[i]);
+  }
+}
+
+// ---- the waves split N ---------------------------------------------------------------------------
+
+// A block of A in LDS: rows of 128 values at a pitch of 272 bytes, which puts the 16 rows of a fragment read on
+// 16 different groups of four banks.  Its values lie in decode's order.
+constexpr int kW4Pitch = 272;
+
+// For more rows: a workgroup owns 16·FM rows and 64·FN columns, a wave 16·FN of them over the whole of K.  A's
+// blocks go through LDS (a block is read once for the workgroup, and put into decode's order once), and so do
+// the scales and zeros, as fp32 pairs; two buffers in turn with one barrier a block.  The codes go straight to
+// the registers of the wave that owns their columns, three blocks ahead: they come from memory, the others
+// mostly from the caches.
+template <int IN, bool ZEROS, int G, int FM, int FN, int PER>
+__global__ void __launch_bounds__(256, PER) gemm_w4_panel_kernel(W4Params p) {
+  constexpr int D = 4, Ahead = FM == 1 ? 2 : 1, Columns = 64 * FN, Groups = kW4Block / G, Pairs = Groups * Columns, Each = (Pairs + 255) / 256;
+  __shared__ __attribute__((aligned(16))) uint8_t panel[2][16 * FM * kW4Pitch];
+  __shared__ W4Scale pair[2][Pairs];
+  const GroupedParams& g = p.g;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), quarter = lane >> 4;
+  RaggedTile t;
+  if (!w4_tile<16 * FM>(g, t)) return;
+  const int first = t.tn * Columns, n0 = first + wave * 16 * FN;
+  const int blocks = (g.K + kW4Block - 1) / kW4Block, last = blocks - 1, left = g.K % kW4Block / 32;
+  // Steps of 32 of block c.  What does not exist of the last block repeats what exists when it is loaded and is
+  // cleared on its way into LDS (so that nothing waits for a load where it is issued).
+  auto steps_of = [&](int c) __attribute__((always_inline)) { return c < last || left == 0 ? 4 : left; };
+
+  // thread i copies 16 bytes of rows i/16, i/16 + 16, ... of A
+  const int chunk = threadIdx.x & 15;
+  const uint8_t* a[FM];
 #pragma unroll
-      for (int n = 0; n < FN; ++n) part[wave][m * FN + n][lane] = acc[m][n];
-    __syncthreads();
+  for (int m = 0; m < FM; ++m)
+    a[m] = g.A + w4_row(p, t.row0 + min(16 * m + (int)(threadIdx.x >> 4), t.rows - 1)) * g.lda;
+  const int to = (threadIdx.x >> 4) * kW4Pitch + chunk * 16, from = (lane & 15) * kW4Pitch + quarter * 16;
+  W4Raw16 next[Ahead][FM];
+  auto load_a = [&](int c, int slot) __attribute__((always_inline)) {
+    c = min(c, last);
+    const uint32_t at = chunk < 4 * steps_of(c) ? chunk * 16 : 0;
 #pragma unroll
-    for (int i = 0; i < Each; ++i) {
-      const int e = threadIdx.x + 64 * W * i, r = e / (16 * FN), n = e % (16 * FN);
-      const int at = (((r >> 4) * FN + (n >> 4)) * 64 + ((r & 15) >> 2) * 16 + (n & 15)) * 4 + (r & 3);
-      x[i] = 0.f;
+    for (int m = 0; m < FM; ++m) next[slot][m] = *(const W4Raw16*)(a[m] + ((int64_t)c * 256 + at));
+  };
+  auto store_a = [&](int c, int slot) __attribute__((always_inline)) {
+    if (left > 0 && c >= last && chunk >= 4 * left) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) x[i] += ((const float*)part[w])[at];
+      for (int m = 0; m < FM; ++m) next[slot][m] = W4Raw16{{0, 0, 0, 0}};
+    }
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      const W4Raw16& r = next[slot][m];
+      *(bf16x8_t*)(panel[c & 1] + 16 * m * kW4Pitch + to) = order_a<IN>(u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]});
     }
   };
-  compute(std::false_type{});
+
+  // and pairs i, i + 256, ... of the groups' scales and zeros
+  const uint8_t* const s_base = (const uint8_t*)(p.scales + (int64_t)t.group * p.stride_s + first);
+  const uint8_t* const z_base = ZEROS ? p.zeros + (int64_t)t.group * p.stride_z + first : nullptr;
+  uint16_t s_next[2][Each];
+  uint8_t z_next[2][Each];
+  // lane offsets of a pair, and of the block's first group, which stands in for one that does not exist
+  uint32_t at_s[Each], at_z[Each], col[Each];
+#pragma unroll
+  for (int e = 0; e < Each; ++e) {
+    const uint32_t i = threadIdx.x + 256 * e, of = i / Columns % Groups;
+    col[e] = min(i % Columns, (uint32_t)(g.N - 1 - first));
+    at_s[e] = of * (uint32_t)(2 * p.ld_s) + 2 * col[e];
+    at_z[e] = of * (uint32_t)p.ld_z + col[e];
+  }
+  auto load_s = [&](int c, int slot) __attribute__((always_inline)) {
+    c = min(c, last);
+    const int steps = steps_of(c);
+    const uint8_t *s = s_base + (int64_t)c * (Groups * 2 * p.ld_s), *z = z_base + (int64_t)c * (Groups * p.ld_z);
+#pragma unroll
+    for (int e = 0; e < Each; ++e) {
+      const bool in = (int)((threadIdx.x + 256 * e) / Columns) * (G / 32) < steps;
+      s_next[slot][e] = *(const uint16_t*)(s + (in ? at_s[e] : 2 * col[e]));
+      if (ZEROS) z_next[slot][e] = z[in ? at_z[e] : col[e]];
+    }
+  };
+  auto store_s = [&](int c, int slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < Each; ++e) {
+      const int i = threadIdx.x + 256 * e;
+      float s = scale_value<IN>(s_next[slot][e]);
+      if (left > 0 && c >= last && i / Columns * (G / 32) >= left) s = 0.f;
+      if (Pairs % 256 == 0 || i < Pairs) pair[c & 1][i] = W4Scale{s, ZEROS ? (float)z_next[slot][e] : 8.f};
+    }
+  };
+
+  const W4Columns<FN> l = w4_columns<FN>(p, t.group, min(n0, g.N - 1), lane);
+  u32x4_t b[D][FN];
+  auto load_b = [&](int d, int c) __attribute__((always_inline)) {
+    c = min(c, last);
+    const uint8_t* base = l.b + (int64_t)c * 64;
+    const uint32_t q = quarter < steps_of(c) ? quarter * 16 : 0;
+#pragma unroll
+    for (int n = 0; n < FN; ++n) b[d][n] = *(const u32x4_t*)(base + (l.at_b[n] + q));
+  };
+
+  f32x4_t acc[FM][FN];
+  clear_sums(acc);
+  auto step = [&](int c, int d) __attribute__((always_inline)) {
+    load_a(c + Ahead, d % Ahead);
+    load_s(c + 2, d & 1);
+    load_b((d + D - 1) % D, c + D - 1);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // block c is in LDS
+    const uint8_t* at = panel[c & 1] + from;
+    const W4Scale* sz = pair[c & 1] + wave * 16 * FN + (lane & 15);
+    block_products<IN, false, G>(acc, b[d], [&](int m, int j) __attribute__((always_inline)) {
+      return *(const bf16x8_t*)(at + 16 * m * kW4Pitch + j * 64);
+    }, [&](int g, int n) __attribute__((always_inline)) { return sz[g * Columns + 16 * n]; });
+    // the last readers of the other buffers passed the barrier above
+    store_a(c + 1, (d + 1) % Ahead);
+    store_s(c + 1, (d + 1) & 1);
+  };
+  if (blocks > 0) {
+    load_a(0, 0);
+    load_s(0, 0);
+    if (Ahead == 2) load_a(1, 1);
+    load_s(1, 1);
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) load_b(d, d);
+    store_a(0, 0);
+    store_s(0, 0);
+    int c = 0;
+    for (; c + D <= blocks; c += D)
+#pragma unroll
+      for (int d = 0; d < D; ++d) step(c + d, d);
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+      if (c + d < blocks) step(c + d, d);
+  }
   if constexpr (IN == 0) {
     bool finite = true;
 #pragma unroll
-    for (int i = 0; i < Each; ++i) finite = finite && fabsf(x[i]) <= 3.4028235e38f;
-    if (__syncthreads_or(!finite)) compute(std::true_type{});
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) finite = finite && is_finite(acc[m][n][i]);
+    if (__ballot(!finite) != 0) {  // the wave's own columns
+#pragma unroll 1
+      for (int f = 0; f < FM * FN; ++f)
+        if (n0 + f % FN * 16 < g.N) w4_exact_fragment<IN, ZEROS, G>(p, t, f / FN * 16, n0 + f % FN * 16);
+      return;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < Each; ++i) {
-    const int e = threadIdx.x + 64 * W * i, r = e / (16 * FN), n = n0 + e % (16 * FN);
-    if (r >= t.rows || n >= g.N) continue;
-    const int64_t at = (int64_t)(t.row0 + r) * g.ldc + n;
-    typedef typename Half4<IN == 1 ? 2 : 1>::elem half;
-    float v = x[i];
-    if (g.scaled) {
-      v *= g.alpha;
-      if (g.beta != 0.f) v = fmaf(g.beta, p.out16 ? (float)((const half*)g.C)[at] : ((const float*)g.C)[at], v);
-    }
-    if (p.out16) ((half*)g.C)[at] = (half)v;
-    else ((float*)g.C)[at] = v;
-  }
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 16 * m + 4 * quarter + i, col = n0 + 16 * n + (lane & 15);
+        if (r < t.rows && col < g.N) w4_store<IN>(p, t.row0 + r, col, acc[m][n][i]);
+      }
 }
 
 }  // namespace tbg

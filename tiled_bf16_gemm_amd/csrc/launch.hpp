@@ -174,15 +174,18 @@ hipError_t launch_few_rows(Mx4GemmParams p, const TileChoice& c, int fmt, int ou
 struct W4Params {
   GroupedParams g;
   const uint16_t* scales;
-  const uint8_t* zeros;   // null: every zero is 8
+  const uint8_t* zeros;   // null in the launchers without zeros
   int64_t ld_s, stride_s, ld_z, stride_z;
   const int32_t* source;  // null, or row r reads row source[r] / top_k of A's a_rows
   FastDiv top_k;
   int a_rows;
   int out16;              // C has A's type, else fp32
 };
-// in: 0 bf16, 1 fp16; group 32, 64 or 128
-hipError_t launch_w4_gemm(W4Params p, int in, int group, const TileChoice& c, hipStream_t stream);
+// By A's type and whether zeros are given; group 32, 64 or 128; the tile counts come from `c`.
+hipError_t launch_w4_bf16(const W4Params& p, int group, const TileChoice& c, hipStream_t stream);
+hipError_t launch_w4_bf16_zeros(const W4Params& p, int group, const TileChoice& c, hipStream_t stream);
+hipError_t launch_w4_f16(const W4Params& p, int group, const TileChoice& c, hipStream_t stream);
+hipError_t launch_w4_f16_zeros(const W4Params& p, int group, const TileChoice& c, hipStream_t stream);
 
 // fp8 GEMM (gemm_fp8.hpp): p in units of two fp8 values (lda, ldb, K, kchunks as for 16-bit data
 // of half the width); fmt 0 E4M3, 1 E5M2; tiles 256×256, 128×128, 64×64.
