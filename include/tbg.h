@@ -629,8 +629,7 @@ tbg_status tbg_expert_combine_grad(int64_t tokens, int64_t top_k, int64_t rows, 
  * elements) and a weight matrix as above; C TBG_F32 or A's type, ldc >= N.
  * Per group the sum of A times whole numbers is held in fp32, multiplied by the scale and added in fp32;
  * nothing else is rounded before C, once, to nearest even.  alpha, beta as tbg_gemm_ex.  Made for few rows
- * (the bytes of W are the cost); any number is taken.  Codes are read to whole 16 bytes, scales and zeros only
- * inside the matrix.
+ * (the bytes of W are the cost); any number is taken.
  * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.
  * Limits: M up to 2^30, ldb below 2^23 (K up to 2^24 - 32), ld_s and ld_z up to 2^28 (N too), workgroups as for the
  * ragged products.

@@ -16,8 +16,8 @@ constexpr int64_t kSmallSlots = 4096;
 inline SortPlan plan_expert_sort(int64_t slots, int64_t groups) {
   SortPlan s{true, 1, slots, 0};
   // one workgroup holds four slots a thread, and has fewer waves the more experts there are
-  int64_t waves = groups > 0 ? 8192 / groups : 16;
-  waves = waves < 16 ? waves : 16;
+  int64_t waves = 16;
+  while (waves > 1 && waves * groups > 8192) waves /= 2;
   if (slots <= waves * 256 && slots <= kSmallSlots) return s;
   s.small = false;
   const int64_t step = 2048, most = 256;

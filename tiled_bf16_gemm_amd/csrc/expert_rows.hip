@@ -21,7 +21,7 @@ namespace tbg {
 namespace {
 
 // 16 bytes of a row, which may start at any byte (gfx9 takes unaligned multi-dword accesses).
-struct __attribute__((packed, aligned(1))) Raw16 { uint32_t w[4]; };
+typedef uint32_t Raw16 __attribute__((ext_vector_type(4), aligned(1)));
 
 // Values of a type: 0 fp32, 1 bf16, 2 fp16.
 template <int DT> struct Elem;
@@ -29,9 +29,44 @@ template <> struct Elem<0> { typedef float type; };
 template <> struct Elem<1> { typedef __bf16 type; };
 template <> struct Elem<2> { typedef _Float16 type; };
 
-// V consecutive values.
+// V consecutive values at any element's boundary.
 template <int DT, int V>
-struct __attribute__((packed, aligned(sizeof(typename Elem<DT>::type)))) Vec { typename Elem<DT>::type v[V]; };
+struct VecOf {
+  typedef typename Elem<DT>::type type __attribute__((ext_vector_type(V), aligned(sizeof(typename Elem<DT>::type))));
+};
+template <int DT>
+struct VecOf<DT, 1> {
+  typedef typename Elem<DT>::type type;
+};
+template <int DT, int V>
+using Vec = typename VecOf<DT, V>::type;
+
+template <int DT, int V>
+__device__ __forceinline__ float value_of(const Vec<DT, V>& x, int i) {
+  if constexpr (V == 1) return (float)x;
+  else return (float)x[i];
+}
+template <int DT, int V>
+__device__ __forceinline__ void set_value(Vec<DT, V>& x, int i, float f) {
+  if constexpr (V == 1) x = (typename Elem<DT>::type)f;
+  else x[i] = (typename Elem<DT>::type)f;
+}
+
+// Rows of the groups that the last-level cache cannot hold are read and written past it (NT), which leaves
+// it to the rest; those that fit may still be in it, or be read from it next.  launch_* choose by kCacheBytes.
+// (O names the type, O::type, so that its alignment stays with it.)
+template <int NT, class O>
+__device__ __forceinline__ typename O::type load_from(const uint8_t* at) {
+  typedef typename O::type T;
+  if constexpr (NT != 0) return __builtin_nontemporal_load((const T*)at);
+  else return *(const T*)at;
+}
+template <int NT, class O>
+__device__ __forceinline__ void store_to(uint8_t* at, typename O::type v) {
+  typedef typename O::type T;
+  if constexpr (NT != 0) __builtin_nontemporal_store(v, (T*)at);
+  else *(T*)at = v;
+}
 
 // The first column of a unit: the last unit of a row ends with the row.
 template <int V>
@@ -47,8 +82,8 @@ template <> struct Unit<1> { typedef uint8_t type; };
 template <> struct Unit<2> { typedef uint16_t type; };
 template <> struct Unit<4> { typedef uint32_t type; };
 
-// SHORT 0: units of 16 bytes; else rows below 16 bytes, one element of SHORT bytes a unit.
-template <int SHORT>
+// SHORT 0: units of 16 bytes; else rows below 16 bytes, one element of SHORT bytes a unit.  J: rows in flight.
+template <int SHORT, int J, int NT>
 __global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
   if (i >= p.units) return;
@@ -56,18 +91,23 @@ __global__ void __launch_bounds__(256) dispatch_kernel(RowsParams p) {
   constexpr int Bytes = SHORT ? SHORT : 16;
   typedef typename Unit<SHORT>::type T;
   const int64_t at = unit_column<Bytes>(u, p.cols);  // cols and columns count bytes here
-  const T v = *(const T*)(p.in + (int64_t)t * p.ld_in + at);
   const int32_t* place = p.place + (int64_t)t * p.top_k;
-  for (uint32_t j = 0; j < p.top_k; ++j) {
-    const uint32_t row = (uint32_t)place[j];
-    if (row < p.rows) *(T*)(p.out + (int64_t)row * p.ld_out + at) = v;
+  const T v = *(const T*)(p.in + (int64_t)t * p.ld_in + at);
+  uint8_t* out = p.out + at;
+  for (uint32_t j0 = 0; j0 < p.top_k; j0 += J) {
+    uint32_t row[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) row[j] = j0 + j < p.top_k ? (uint32_t)place[j0 + j] : ~0u;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (row[j] < p.rows) store_to<NT, Unit<SHORT>>(out + (int64_t)row[j] * p.ld_out, v);
   }
 }
 
 // ---- combine -------------------------------------------------------------------------------------
 
 // Y: type of the rows, O: type of the sum, V: values a unit, J: rows in flight.
-template <int Y, int O, int V, int J>
+template <int Y, int O, int V, int J, int NT>
 __global__ void __launch_bounds__(256) combine_kernel(RowsParams p) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
   if (i >= p.units) return;
@@ -91,17 +131,17 @@ __global__ void __launch_bounds__(256) combine_kernel(RowsParams p) {
     }
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (row[j] < p.rows) y[j] = *(const In*)(in + (int64_t)row[j] * p.ld_in);
+      if (row[j] < p.rows) y[j] = load_from<NT, VecOf<Y, V>>(in + (int64_t)row[j] * p.ld_in);
 #pragma unroll
     for (int j = 0; j < J; ++j)
       if (row[j] < p.rows) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum[v] = fmaf(w[j], (float)y[j].v[v], sum[v]);
+        for (int v = 0; v < V; ++v) sum[v] = fmaf(w[j], value_of<Y, V>(y[j], v), sum[v]);
       }
   }
   Vec<O, V> o;
 #pragma unroll
-  for (int v = 0; v < V; ++v) o.v[v] = (typename Elem<O>::type)sum[v];
+  for (int v = 0; v < V; ++v) set_value<O, V>(o, v, sum[v]);
   *(Vec<O, V>*)(p.out + (int64_t)t * p.ld_out + c * (int64_t)sizeof(typename Elem<O>::type)) = o;
 }
 
@@ -114,7 +154,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // A workgroup of W waves a token; J of its rows at a time.  Y: type of the rows, D: of dout.
-template <int Y, int D, int V, int J, int W>
+template <int Y, int D, int V, int J, int W, int NT>
 __global__ void __launch_bounds__(64 * W) combine_grad_kernel(RowsParams p) {
   __shared__ float part[W][J];
   const uint32_t t = blockIdx.x;
@@ -139,18 +179,19 @@ __global__ void __launch_bounds__(64 * W) combine_grad_kernel(RowsParams p) {
       Vec<Y, V> y[J];
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (row[j] < p.rows) y[j] = *(const Vec<Y, V>*)(p.in + (int64_t)row[j] * p.ld_in + c * (int64_t)sizeof(elem));
+        if (row[j] < p.rows)
+          y[j] = load_from<NT, VecOf<Y, V>>(p.in + (int64_t)row[j] * p.ld_in + c * (int64_t)sizeof(elem));
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if (row[j] >= p.rows) continue;
         Vec<Y, V> g;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float x = (float)d.v[v];
-          dot[j] = v >= shared ? fmaf((float)y[j].v[v], x, dot[j]) : dot[j];
-          g.v[v] = (elem)(w[j] * x);
+          const float x = value_of<D, V>(d, v);
+          dot[j] = v >= shared ? fmaf(value_of<Y, V>(y[j], v), x, dot[j]) : dot[j];
+          set_value<Y, V>(g, v, w[j] * x);
         }
-        *(Vec<Y, V>*)(p.out + (int64_t)row[j] * p.ld_out + c * (int64_t)sizeof(elem)) = g;
+        store_to<NT, VecOf<Y, V>>(p.out + (int64_t)row[j] * p.ld_out + c * (int64_t)sizeof(elem), g);
       }
     }
 #pragma unroll
@@ -171,6 +212,13 @@ __global__ void __launch_bounds__(64 * W) combine_grad_kernel(RowsParams p) {
   }
 }
 
+// Whether the groups' rows fill the last-level cache.
+constexpr int64_t kCacheBytes = 256ll << 20;
+bool past_cache(const RowsParams& p, int size) {
+  const int64_t held = (int64_t)p.tokens * p.top_k;
+  return (held < p.rows ? held : p.rows) * p.cols * size >= kCacheBytes;
+}
+
 // Tokens that one launch takes: their units are numbered in 32 bits.
 template <class Launch>
 hipError_t by_tokens(const RowsParams& p, Launch launch) {
@@ -189,15 +237,32 @@ hipError_t by_tokens(const RowsParams& p, Launch launch) {
   return hipSuccess;
 }
 
+template <int SHORT>
+hipError_t dispatch_units(RowsParams p, hipStream_t s) {
+  constexpr int Bytes = SHORT ? SHORT : 16;
+  p.per_row = (uint32_t)((p.cols + Bytes - 1) / Bytes);
+  p.div = make_fast_div(p.per_row);
+  return by_tokens(p, [&](RowsParams q, int64_t t, unsigned grid) {
+    q.in += t * p.ld_in;
+    // 8192 tokens of 8 KiB, 8 rows each (512 MiB): 126 µs, past the cache 107; 2 rows each (128 MiB): 28 either way
+    if (p.top_k <= 2) hipLaunchKernelGGL((dispatch_kernel<SHORT, 2, 0>), dim3(grid), dim3(256), 0, s, q);
+    else if (!past_cache(p, 1)) hipLaunchKernelGGL((dispatch_kernel<SHORT, 8, 0>), dim3(grid), dim3(256), 0, s, q);
+    else hipLaunchKernelGGL((dispatch_kernel<SHORT, 8, 1>), dim3(grid), dim3(256), 0, s, q);
+  });
+}
+
 template <int Y, int O, int V>
 hipError_t combine_units(RowsParams p, hipStream_t s) {
   p.per_row = (uint32_t)((p.cols + V - 1) / V);
   p.div = make_fast_div(p.per_row);
   return by_tokens(p, [&](RowsParams q, int64_t t, unsigned grid) {
     q.out += t * p.ld_out;
-    if (p.top_k <= 2) hipLaunchKernelGGL((combine_kernel<Y, O, V, 2>), dim3(grid), dim3(256), 0, s, q);
-    else if (p.top_k <= 4) hipLaunchKernelGGL((combine_kernel<Y, O, V, 4>), dim3(grid), dim3(256), 0, s, q);
-    else hipLaunchKernelGGL((combine_kernel<Y, O, V, 8>), dim3(grid), dim3(256), 0, s, q);
+    // 8192 tokens of 8 KiB, 8 rows each (512 MiB): 126 µs, past the cache 109; 2 rows each (128 MiB): 34 and 35
+    const bool past = past_cache(p, (int)sizeof(typename Elem<Y>::type));
+    if (p.top_k <= 2) hipLaunchKernelGGL((combine_kernel<Y, O, V, 2, 0>), dim3(grid), dim3(256), 0, s, q);
+    else if (p.top_k <= 4) hipLaunchKernelGGL((combine_kernel<Y, O, V, 4, 0>), dim3(grid), dim3(256), 0, s, q);
+    else if (!past) hipLaunchKernelGGL((combine_kernel<Y, O, V, 8, 0>), dim3(grid), dim3(256), 0, s, q);
+    else hipLaunchKernelGGL((combine_kernel<Y, O, V, 8, 1>), dim3(grid), dim3(256), 0, s, q);
   });
 }
 
@@ -207,8 +272,8 @@ hipError_t combine_types(const RowsParams& p, hipStream_t s) {
   return p.cols >= V ? combine_units<Y, O, V>(p, s) : combine_units<Y, O, 1>(p, s);
 }
 
-template <int Y, int D, int V, int J>
-hipError_t grad_rows(const RowsParams& p, hipStream_t s) {
+template <int Y, int D, int V, int J, int W, int NT>
+hipError_t grad_launch(const RowsParams& p, hipStream_t s) {
   const int64_t most = (1 << 22) - 1;  // workgroups of 256 threads a launch, counted in 32 bits
   for (int64_t t = 0; t < p.tokens; t += most) {
     const int64_t n = p.tokens - t < most ? p.tokens - t : most;
@@ -217,11 +282,21 @@ hipError_t grad_rows(const RowsParams& p, hipStream_t s) {
     q.place += t * p.top_k;
     if (q.weights) q.weights += t * p.top_k;
     q.dweights += t * p.top_k;
-    hipLaunchKernelGGL((combine_grad_kernel<Y, D, V, J, 4>), dim3((unsigned)n), dim3(256), 0, s, q);
+    hipLaunchKernelGGL((combine_grad_kernel<Y, D, V, J, W, NT>), dim3((unsigned)n), dim3(64 * W), 0, s, q);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// Waves a token: one for rows of up to 128 units (2047 tokens, 4 rows of 126 units each: 9.9 µs with one wave, 10.2
+// with two, 11.3 with four), else four (8192 tokens, 2 rows of 512 units: 71, 68, 67).  Past the cache by the rows
+// of Y and dY together: 8192 tokens of 8 KiB, 2 rows each (256 MiB): 67 µs, past the cache 53.
+template <int Y, int D, int V, int J>
+hipError_t grad_rows(const RowsParams& p, hipStream_t s) {
+  if (p.per_row <= 128) return grad_launch<Y, D, V, J, 1, 0>(p, s);
+  if (!past_cache(p, 2 * (int)sizeof(typename Elem<Y>::type))) return grad_launch<Y, D, V, J, 4, 0>(p, s);
+  return grad_launch<Y, D, V, J, 4, 1>(p, s);
 }
 
 template <int Y, int D, int V>
@@ -242,16 +317,9 @@ hipError_t grad_types(const RowsParams& p, hipStream_t s) {
 
 hipError_t launch_expert_dispatch(RowsParams p, int size, hipStream_t stream) {
   p.cols *= size;
-  const int unit = p.cols >= 16 ? 16 : size;
-  p.per_row = (uint32_t)((p.cols + unit - 1) / unit);
-  p.div = make_fast_div(p.per_row);
-  return by_tokens(p, [&](RowsParams q, int64_t t, unsigned grid) {
-    q.in += t * p.ld_in;
-    if (unit == 16) hipLaunchKernelGGL((dispatch_kernel<0>), dim3(grid), dim3(256), 0, stream, q);
-    else if (unit == 4) hipLaunchKernelGGL((dispatch_kernel<4>), dim3(grid), dim3(256), 0, stream, q);
-    else if (unit == 2) hipLaunchKernelGGL((dispatch_kernel<2>), dim3(grid), dim3(256), 0, stream, q);
-    else hipLaunchKernelGGL((dispatch_kernel<1>), dim3(grid), dim3(256), 0, stream, q);
-  });
+  if (p.cols >= 16) return dispatch_units<0>(p, stream);
+  if (size == 4) return dispatch_units<4>(p, stream);
+  return size == 2 ? dispatch_units<2>(p, stream) : dispatch_units<1>(p, stream);
 }
 
 hipError_t launch_expert_combine(RowsParams p, int y, int out, hipStream_t stream) {

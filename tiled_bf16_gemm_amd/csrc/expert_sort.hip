@@ -25,8 +25,10 @@ namespace tbg {
 namespace {
 
 constexpr int kMostWaves = 16;
-constexpr int kWaveCounters = 8192;  // 16-bit counters of all waves: E <= 512 has 16 waves, E = 4096 two
+constexpr int kWaveCounters = 8192;  // 16-bit counters of all waves, an id's side by side: up to 512 ids have 16
+                                     // waves, 4096 two
 constexpr int kMostGroups = 4096;
+constexpr int kAhead = 16;  // values of the table that a thread asks for before it ranks its slots
 
 // Lanes whose slot has this lane's id (among the lanes with `held`; e is below 2^bits).
 __device__ __forceinline__ uint64_t peers(int e, bool held, int bits) {
@@ -84,52 +86,63 @@ __device__ __forceinline__ void load_ids(Step<I>& s, const SortParams& p, int64_
   }
 }
 
-// Ranks, and the wave's counters (`mine`, zero before) with its slots of every id.
+// Ranks, and the wave's counters (zero before; id e's at mine[e * waves]) with its slots of every id.
 template <int I>
-__device__ __forceinline__ void rank_ids(Step<I>& s, uint16_t* mine, int bits) {
+__device__ __forceinline__ void rank_ids(Step<I>& s, uint16_t* mine, int waves, int bits) {
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const bool held = s.id[i] >= 0;
     const uint64_t m = peers(s.id[i], held, bits);
-    const int before = held ? mine[s.id[i]] : 0;
+    uint16_t* const count = mine + (held ? s.id[i] * waves : 0);
+    const int before = held ? *count : 0;
     const int rank = lanes_before(m), all = __popcll(m);
     s.rank[i] = before + rank;
     // the reads of this 64 come before the writes, those before the next 64's reads: one wave's LDS
     // accesses complete in order, and the fences keep the compiler's order
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (held && rank == all - 1) mine[s.id[i]] = (uint16_t)(before + all);
+    if (held && rank == all - 1) *count = (uint16_t)(before + all);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-// The waves' counters become the counts of the waves before; sums[e] gets (or adds) the step's count.
-template <bool ADD>
+// The waves' counters become the counts of the waves before; sums[e] gets the step's count.  (An id's counters lie
+// side by side, two to a dword: with a wave's side by side this took a dependent read and write for every wave.)
 __device__ __forceinline__ void sum_waves(uint16_t* counters, int* sums, int E) {
   const int waves = blockDim.x >> 6;
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int run = 0;
-    for (int w = 0; w < waves; ++w) {
-      const int n = counters[w * E + e];
-      counters[w * E + e] = (uint16_t)run;
-      run += n;
+    if (waves == 1) {
+      sums[e] = counters[e];
+      counters[e] = 0;
+      continue;
     }
-    sums[e] = ADD ? sums[e] + run : run;
+    uint32_t* const pairs = (uint32_t*)(counters + e * waves);
+    uint32_t v[kMostWaves / 2];
+#pragma unroll
+    for (int w = 0; w < kMostWaves / 2; ++w) v[w] = 2 * w < waves ? pairs[w] : 0;
+    uint32_t run = 0;
+#pragma unroll
+    for (int w = 0; w < kMostWaves / 2; ++w) {
+      const uint32_t lo = v[w] & 0xFFFFu, hi = v[w] >> 16;
+      if (2 * w < waves) pairs[w] = run | (run + lo) << 16;
+      run += lo + hi;
+    }
+    sums[e] = (int)run;
   }
 }
 
 // The step's rows, base[e] being the first of id e.
 template <int I>
 __device__ __forceinline__ void store_step(const Step<I>& s, const SortParams& p, int64_t first, int64_t end,
-                                           const uint16_t* mine, const int* base) {
+                                           const uint16_t* mine, int waves, const int* base) {
   const int64_t at = first + (threadIdx.x >> 6) * (64 * I) + (threadIdx.x & 63);
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     if (at + 64 * i >= end) break;
     int row = -1;
     if (s.id[i] >= 0) {
-      row = base[s.id[i]] + mine[s.id[i]] + s.rank[i];
+      row = base[s.id[i]] + mine[s.id[i] * waves] + s.rank[i];
       p.source[row] = (int)(at + 64 * i);
     }
     p.place[at + 64 * i] = row;
@@ -147,18 +160,19 @@ __global__ void __launch_bounds__(64 * kMostWaves) sort_small_kernel(SortParams 
   __shared__ int base[kMostGroups + 1];
   __shared__ int part[kMostWaves];
   const int E = p.groups;
-  uint16_t* mine = counters + (threadIdx.x >> 6) * E;
+  const int waves = blockDim.x >> 6;
+  uint16_t* mine = counters + (threadIdx.x >> 6);
   Step<I> s;
   load_ids(s, p, 0, p.slots);
   clear_counters(counters, E);
   __syncthreads();
-  rank_ids(s, mine, p.bits);
+  rank_ids(s, mine, waves, p.bits);
   __syncthreads();
-  sum_waves<false>(counters, base, E);
+  sum_waves(counters, base, E);
   __syncthreads();
   scan_groups(base, part, E);
   for (int e = threadIdx.x; e <= E; e += blockDim.x) p.offsets[e] = base[e];
-  store_step(s, p, 0, p.slots, mine, base);
+  store_step(s, p, 0, p.slots, mine, waves, base);
   for (int r = base[E] + threadIdx.x; r < p.slots; r += blockDim.x) p.source[r] = -1;
 }
 
@@ -184,21 +198,44 @@ __global__ void __launch_bounds__(64 * kMostWaves) sort_place_kernel(SortParams 
   __shared__ int before[kMostGroups];
   __shared__ int part[kMostWaves];
   const int E = p.groups, me = blockIdx.x, parts = gridDim.x;
-  uint16_t* mine = counters + (threadIdx.x >> 6) * E;
+  const int waves = blockDim.x >> 6;
+  uint16_t* mine = counters + (threadIdx.x >> 6);
+  const int64_t lo = (int64_t)me * p.part, end = min(lo + p.part, (int64_t)p.slots);
+  const int step = blockDim.x * I;
+  Step<I> s;
+  load_ids(s, p, lo, end);  // on the way while the table is read
+  clear_counters(counters, E);
   for (int e = threadIdx.x; e < E; e += blockDim.x) base[e] = before[e] = 0;
   __syncthreads();
-  // consecutive threads take consecutive ids; the threads beyond E take other parts
+  // Consecutive threads take consecutive ids; the threads beyond E take other parts.  The first kAhead values of a
+  // thread are on the way while the slots are ranked.
   const int lanes = E < (int)blockDim.x ? E : (int)blockDim.x, rows = E ? blockDim.x / lanes : 0;
-  const int row = E ? threadIdx.x / lanes : 0;
-  for (int e = E ? threadIdx.x % lanes : 0; e < E && row < rows; e += lanes) {
+  const int row = E ? threadIdx.x / lanes : 0, e0 = E ? threadIdx.x % lanes : 0;
+  int ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int b = row + i * rows;
+    ahead[i] = e0 < E && row < rows && b < parts ? p.table[(int64_t)b * E + e0] : 0;
+  }
+  rank_ids(s, mine, waves, p.bits);
+  if (e0 < E && row < rows) {
     int all = 0, first = 0;
-    for (int b = row; b < parts; b += rows) {
-      const int n = p.table[(int64_t)b * E + e];
-      all += n;
-      first += b < me ? n : 0;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      all += ahead[i];
+      first += row + i * rows < me ? ahead[i] : 0;
     }
-    atomicAdd(&base[e], all);
-    atomicAdd(&before[e], first);
+    for (int e = e0, from = row + kAhead * rows; e < E; e += lanes, from = row) {
+#pragma unroll 8
+      for (int b = from; b < parts; b += rows) {
+        const int n = p.table[(int64_t)b * E + e];
+        all += n;
+        first += b < me ? n : 0;
+      }
+      atomicAdd(&base[e], all);
+      atomicAdd(&before[e], first);
+      all = first = 0;
+    }
   }
   __syncthreads();
   scan_groups(base, part, E);
@@ -207,29 +244,29 @@ __global__ void __launch_bounds__(64 * kMostWaves) sort_place_kernel(SortParams 
   const int filled = base[E];
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) base[e] += before[e];
-  const int64_t lo = (int64_t)me * p.part, end = min(lo + p.part, (int64_t)p.slots);
-  const int step = blockDim.x * I;
   for (int64_t first = lo; first < end; first += step) {
-    Step<I> s;
-    load_ids(s, p, first, end);
-    clear_counters(counters, E);
-    __syncthreads();
-    rank_ids(s, mine, p.bits);
-    __syncthreads();
-    sum_waves<false>(counters, before, E);
-    __syncthreads();
-    store_step(s, p, first, end, mine, base);
-    if (first + step < end) {
-      __syncthreads();
+    if (first > lo) {
       for (int e = threadIdx.x; e < E; e += blockDim.x) base[e] += before[e];
+      clear_counters(counters, E);
+      load_ids(s, p, first, end);
     }
+    if (first > lo) {
+      __syncthreads();
+      rank_ids(s, mine, waves, p.bits);
+    }
+    __syncthreads();
+    sum_waves(counters, before, E);
+    __syncthreads();
+    store_step(s, p, first, end, mine, waves, base);
+    if (first + step < end) __syncthreads();
   }
   for (int64_t r = filled + lo + threadIdx.x; r < p.slots && r < filled + end; r += blockDim.x) p.source[r] = -1;
 }
 
 int waves_for(int groups) {
-  int w = groups > 0 ? kWaveCounters / groups : kMostWaves;
-  return w < kMostWaves ? w : kMostWaves;
+  int w = kMostWaves;  // a power of two: an id's counters are whole dwords, or one
+  while (w > 1 && w * groups > kWaveCounters) w /= 2;
+  return w;
 }
 
 }  // namespace
@@ -241,8 +278,8 @@ hipError_t launch_expert_sort(SortParams p, const SortPlan& plan, hipStream_t st
   const int most = 64 * waves_for(p.groups);
   if (plan.small) {
     const int want = p.slots > p.groups ? p.slots : p.groups;
-    int threads = (want + 63) / 64 * 64;
-    threads = threads < 64 ? 64 : threads < most ? threads : most;
+    int threads = 64;
+    while (threads < want && threads < most) threads *= 2;
     if (p.slots <= threads) hipLaunchKernelGGL((sort_small_kernel<1>), dim3(1), dim3(threads), 0, stream, p);
     else hipLaunchKernelGGL((sort_small_kernel<4>), dim3(1), dim3(threads), 0, stream, p);
     return hipGetLastError();
