@@ -188,7 +188,9 @@ inline TileChoice choose_mx4(int64_t groups, int64_t M, int64_t N, int64_t K, in
 //    32 × 14336   39.6  28.4  20.9   20.7  25.6  35.7       256 × 14336    280   172   118   80.2  66.0  55.9
 // 64 groups, 64 rows (8 of 64 experts for 8 tokens), N = 4096, K = 2048: 64.3, 50.6, 46.7; 41.7, 48.5, 76.6;
 // 2008 rows, N = 2048, K = 4096, group 64 with zeros: 393, 250, 184; 143, 135, 163.
-inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, int cus) {
+// Split K over 64 columns is not built for groups of 32 with zeros, whose scales and zeros do not fit the registers
+// (`wide` false; 16 × 14336: 25.4, 18.3 and, spilled, 23.1).
+inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, bool wide, int cus) {
   TileChoice c{};
   const double active = groups > 0 ? (double)(groups < M ? groups : M) : 1.0, rows = (double)M / active;
   auto tiles = [&](int bm, int bn) {  // ragged groups of the average size, each ending half way into its last tile
@@ -199,7 +201,7 @@ inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, int cus) {
   c.few = tiles(16, 128) < most;
   if (c.few) {
     c.bm = 16;
-    c.bn = tiles(16, 64) >= most ? 64 : tiles(16, 32) >= most ? 32 : 16;
+    c.bn = wide && tiles(16, 64) >= most ? 64 : tiles(16, 32) >= most ? 32 : 16;
   } else {
     c.bm = rows > 32 && tiles(64, 128) >= most ? 64 : rows > 16 && tiles(32, 128) >= most ? 32 : 16;
     c.bn = 128;
