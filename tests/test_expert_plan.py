@@ -37,9 +37,9 @@ static void splits(int64_t groups, int64_t M, int64_t N) {
     sizes[next(groups)] += n;
     left -= n;
   }
-  for (int kind = 0; kind < 4; ++kind) {
-    const bool ragged = kind & 1, wide = kind & 2;
-    const TileChoice c = choose_w4(ragged ? groups : 0, M, N, wide, 256);
+  for (int kind = 0; kind < 2; ++kind) {
+    const bool ragged = kind & 1;
+    const TileChoice c = choose_w4(ragged ? groups : 0, M, N, 256);
     int64_t rows = 0;
     if (ragged) for (int64_t n : sizes) rows += tile_count(n, c.bm);
     else rows = tile_count(M, c.bm);
@@ -48,7 +48,6 @@ static void splits(int64_t groups, int64_t M, int64_t N) {
     CHECK(c.grid % 8 == 0 && c.grid >= c.tiles_m * c.tiles_n && c.fits(), "M %lld", (long long)M);
     CHECK(c.few ? c.bm == 16 && (c.bn == 16 || c.bn == 32 || c.bn == 64) : c.bn == 128 && (c.bm == 16 || c.bm == 32 || c.bm == 64),
           "%d x %d", c.bm, c.bn);
-    CHECK(wide || !(c.few && c.bn == 64), "N %lld", (long long)N);
   }
 }
 
@@ -59,10 +58,10 @@ int main() {
   for (int i = 0; i < 20000; ++i) splits(spread(200), spread(9000), spread(20000));
   // the most workgroups of one launch, and one tile more
   const int64_t most = (1 << 24) - 1, up = most / 8 * 8;
-  CHECK(choose_w4(0, 64 * up, 128, true, 256).fits(), "dense");
-  CHECK(!choose_w4(0, 64 * up + 1, 128, true, 256).fits(), "dense");
-  CHECK(choose_w4(1, 64, 128 * up, true, 256).fits(), "ragged");
-  CHECK(!choose_w4(1, 64, 128 * up + 1, true, 256).fits(), "ragged");
+  CHECK(choose_w4(0, 64 * up, 128, 256).fits(), "dense");
+  CHECK(!choose_w4(0, 64 * up + 1, 128, 256).fits(), "dense");
+  CHECK(choose_w4(1, 64, 128 * up, 256).fits(), "ragged");
+  CHECK(!choose_w4(1, 64, 128 * up + 1, 256).fits(), "ragged");
   std::printf("%s\n", bad ? "bad" : "ok");
   return bad != 0;
 }

@@ -163,7 +163,7 @@ def _bound(a, code, s, z, exact, out):
 
 SHAPES = [(1, 1, 32, 32), (1, 16, 128, 128), (3, 17, 96, 32), (16, 64, 256, 64), (5, 100, 192, 64), (17, 33, 640, 128),
           (33, 257, 544, 32), (64, 48, 1152, 128), (65, 130, 2048, 64), (130, 20, 4096, 128), (2, 5000, 160, 32),
-          (20, 9000, 128, 128), (40, 9001, 64, 64), (7, 15, 8192, 32), (40, 14400, 160, 32), (200, 6200, 192, 64),
+          (20, 9000, 128, 128), (40, 9001, 64, 64), (7, 15, 8192, 32), (40, 16400, 160, 32), (200, 6200, 192, 64),
           (100, 12300, 384, 128)]
 
 
@@ -230,7 +230,7 @@ def test_order_of_the_codes():
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("M,N", [(5, 24700), (30, 24700), (60, 24700), (9, 400), (9, 7000), (9, 12400)])
+@pytest.mark.parametrize("M,N", [(5, 32800), (30, 32800), (60, 32800), (9, 400), (9, 7000), (9, 12400)])
 def test_every_number_of_blocks(M, N, dtype):
     """Each kernel over sums of less than one block of 128 up to nine, whole or not."""
     ops = _ops()
@@ -244,7 +244,7 @@ def test_every_number_of_blocks(M, N, dtype):
 
 
 @gpu
-@pytest.mark.parametrize("M,N,K", [(40, 70, 512), (40, 24700, 256), (30, 24700, 160), (16, 24700, 96), (16, 12400, 160)])
+@pytest.mark.parametrize("M,N,K", [(40, 70, 512), (40, 32800, 256), (30, 32800, 160), (16, 32800, 96), (16, 12400, 160)])
 def test_infinities_and_huge_values(M, N, K):
     """Rows that hold an infinity, a NaN or values near the end of bf16's range come out as the definition's sum, and
     the others are not touched by them."""

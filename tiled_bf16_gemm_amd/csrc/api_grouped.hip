@@ -519,7 +519,7 @@ tbg_status w4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t
   int cus = 0;
   st = check_device(&cus);
   if (st != TBG_OK) return st;
-  const tbg::TileChoice choice = tbg::choose_w4(ragged ? groups : 0, M, N, group != 32 || !zeros, cus);
+  const tbg::TileChoice choice = tbg::choose_w4(ragged ? groups : 0, M, N, cus);
   st = check_grid(choice);
   if (st != TBG_OK) return st;
   tbg::W4Params p;

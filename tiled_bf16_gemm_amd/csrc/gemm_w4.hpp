@@ -81,59 +81,64 @@ __device__ __forceinline__ bf16x8_t decode(uint32_t w, float z) {
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
+// Exchanges the upper half of x's lanes with the lower of y's; the odd rows of 16 lanes of x with the even ones of y.
+__device__ __forceinline__ void swap_halves(uint32_t& x, uint32_t& y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  x = r[0];
+  y = r[1];
+}
+__device__ __forceinline__ void swap_rows(uint32_t& x, uint32_t& y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  x = r[0];
+  y = r[1];
+}
+
 // Dword d of quarter q becomes dword q of quarter d.
 __device__ __forceinline__ void turn_quarters(u32x4_t& b) {
-  auto swap32 = [](uint32_t& x, uint32_t& y) {
-    const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-    x = r[0];
-    y = r[1];
-  };
-  auto swap16 = [](uint32_t& x, uint32_t& y) {
-    const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-    x = r[0];
-    y = r[1];
-  };
   uint32_t r0 = b[0], r1 = b[1], r2 = b[2], r3 = b[3];
-  swap32(r0, r2);
-  swap32(r1, r3);
-  swap16(r0, r1);
-  swap16(r2, r3);
+  swap_halves(r0, r2);
+  swap_halves(r1, r3);
+  swap_rows(r0, r1);
+  swap_rows(r2, r3);
   b = u32x4_t{r0, r1, r2, r3};
 }
 
-// What a wave holds of the weights of a block of 128 codes, FN fragments of columns.
-template <int G, int FN>
+// What a wave holds of the weights of a block of 128 codes, FN fragments of columns: the codes of a lane's column and
+// quarter, and scale and zero of the group that the quarter lies in.
+template <int FN>
 struct W4Weights {
-  static constexpr int Groups = kW4Block / G;
   u32x4_t b[FN];
-  uint16_t s[Groups][FN];
-  uint8_t z[Groups][FN];
+  uint16_t s[FN];
+  uint8_t z[FN];
 };
 
-// Where a lane reads its columns' codes, scales and zeros: from the tile's bases, the same for every lane.
+// Where a lane reads its columns' codes, scales and zeros: offsets from the tile's bases, which are the same for
+// every lane.
 template <int FN>
 struct W4Columns {
-  const uint8_t* b;    // the first column's codes
-  const uint8_t* s;    // its scales
-  const uint8_t* z;    // its zeros
-  int64_t ld_s, ld_z;  // bytes
-  uint32_t at_b[FN], at_s[FN], at_z[FN];
+  const uint8_t* b;  // the first column's codes
+  const uint8_t* s;  // its scales
+  const uint8_t* z;  // its zeros
+  int64_t block_s, block_z;  // bytes from one block's scales (zeros) to the next one's
+  uint32_t group_s, group_z;  // and from one group's
+  uint32_t at_b[FN], col[FN];
 };
 
 // Columns n0, n0 + 1, ... of W_group, the lane's at n0 + 16·n + lane%16.
-template <int FN>
+template <int G, int FN>
 __device__ __forceinline__ W4Columns<FN> w4_columns(const W4Params& p, int group, int n0, int lane) {
   W4Columns<FN> l;
   l.b = p.g.B + (int64_t)group * p.g.stride_b + (int64_t)n0 * p.g.ldb;
   l.s = (const uint8_t*)(p.scales + (int64_t)group * p.stride_s + n0);
   l.z = p.zeros ? p.zeros + (int64_t)group * p.stride_z + n0 : nullptr;
-  l.ld_s = 2 * p.ld_s;
-  l.ld_z = p.ld_z;
+  l.block_s = kW4Block / G * 2 * p.ld_s;
+  l.block_z = kW4Block / G * p.ld_z;
+  l.group_s = (uint32_t)(2 * p.ld_s);
+  l.group_z = (uint32_t)p.ld_z;
 #pragma unroll
   for (int n = 0; n < FN; ++n) {
-    l.at_z[n] = (uint32_t)max(min(16 * n + (lane & 15), p.g.N - 1 - n0), 0);
-    l.at_s[n] = 2 * l.at_z[n];
-    l.at_b[n] = l.at_z[n] * (uint32_t)p.g.ldb;
+    l.col[n] = (uint32_t)max(min(16 * n + (lane & 15), p.g.N - 1 - n0), 0);
+    l.at_b[n] = l.col[n] * (uint32_t)p.g.ldb;
   }
   return l;
 }
@@ -141,20 +146,16 @@ __device__ __forceinline__ W4Columns<FN> w4_columns(const W4Params& p, int group
 // Block c, of which `steps` steps of 32 exist (ALL: four).  What is past them repeats what exists; the products
 // leave it out.  Nothing is computed with what is loaded here, which would wait for it.
 template <bool ALL, bool ZEROS, int G, int FN>
-__device__ __forceinline__ void load_weights(W4Weights<G, FN>& k, const W4Columns<FN>& l, int c, int steps, int quarter) {
-  const uint8_t* b = l.b + (int64_t)c * 64;
-  const uint32_t q = ALL || quarter < steps ? quarter * 16 : 0;
+__device__ __forceinline__ void load_weights(W4Weights<FN>& k, const W4Columns<FN>& l, int c, int steps, int quarter) {
+  const uint8_t *b = l.b + (int64_t)c * 64, *s = l.s + c * l.block_s, *z = l.z + c * l.block_z;
+  const bool in = ALL || quarter < steps;
+  const uint32_t q = in ? quarter * 16 : 0, g = in ? quarter / (G / 32) : 0;
 #pragma unroll
   for (int n = 0; n < FN; ++n) k.b[n] = *(const u32x4_t*)(b + (l.at_b[n] + q));
 #pragma unroll
-  for (int g = 0; g < W4Weights<G, FN>::Groups; ++g) {
-    const int64_t row = (int64_t)c * W4Weights<G, FN>::Groups + (ALL || g * (G / 32) < steps ? g : 0);
-    const uint8_t *s = l.s + row * l.ld_s, *z = l.z + row * l.ld_z;
-#pragma unroll
-    for (int n = 0; n < FN; ++n) {
-      k.s[g][n] = *(const uint16_t*)(s + l.at_s[n]);
-      if (ZEROS) k.z[g][n] = z[l.at_z[n]];
-    }
+  for (int n = 0; n < FN; ++n) {
+    k.s[n] = *(const uint16_t*)(s + (g * l.group_s + 2 * l.col[n]));
+    if (ZEROS) k.z[n] = z[g * l.group_z + l.col[n]];
   }
 }
 
@@ -192,21 +193,44 @@ struct W4Scale {
   float s, z;
 };
 
+// The groups' scales and zeros for every quarter, from the quarters that hold them: a scale and a zero are one dword,
+// whose rows of 16 lanes are copied to the others with the swaps of turn_quarters.  (A load for every group and column
+// would be 16 of 22 loads a block for groups of 32 with zeros and two fragments: 33 × 2049 × 8160 15.7 µs, so 14.3.)
 template <int IN, bool ZEROS, int G, int FN>
-__device__ __forceinline__ auto scales_of(const W4Weights<G, FN>& k) {
-  return [&k](int g, int n) __attribute__((always_inline)) {
-    return W4Scale{scale_value<IN>(k.s[g][n]), ZEROS ? (float)k.z[g][n] : 8.f};
-  };
-}
+struct W4Scales {
+  static constexpr int Groups = kW4Block / G;
+  uint32_t v[Groups][FN];
 
-// Groups of a block from step `steps` on do not exist: their scales count as zero (and A's values as zeros).
+  __device__ __forceinline__ W4Scales(const W4Weights<FN>& k) {
+#pragma unroll
+    for (int n = 0; n < FN; ++n) {
+      uint32_t r[4];
+      r[0] = k.s[n] | (ZEROS ? (uint32_t)k.z[n] << 16 : 0u);
+      if (G == 32) {  // rows 0 0 2 2 and 1 1 3 3
+        r[1] = r[0];
+        swap_rows(r[0], r[1]);
+        r[3] = r[1];
+        swap_halves(r[1], r[3]);
+      }
+      if (G <= 64) {
+        r[2] = r[0];
+        swap_halves(r[0], r[2]);
+      }
+#pragma unroll
+      for (int g = 0; g < Groups; ++g) v[g][n] = r[G == 64 ? 2 * g : g];
+    }
+  }
+  __device__ __forceinline__ W4Scale operator()(int g, int n) const {
+    return W4Scale{scale_value<IN>((uint16_t)v[g][n]), ZEROS ? (float)(v[g][n] >> 16) : 8.f};
+  }
+};
+
+// The lane's group of a block from step `steps` on does not exist: its scale counts as zero (and A's values as zeros).
 template <int G, int FN>
-__device__ __forceinline__ void end_weights(W4Weights<G, FN>& k, int steps) {
+__device__ __forceinline__ void end_weights(W4Weights<FN>& k, int steps, int quarter) {
 #pragma unroll
-  for (int g = 0; g < W4Weights<G, FN>::Groups; ++g)
-#pragma unroll
-    for (int n = 0; n < FN; ++n)
-      if (g * (G / 32) >= steps) k.s[g][n] = 0;
+  for (int n = 0; n < FN; ++n)
+    if (quarter / (G / 32) * (G / 32) >= steps) k.s[n] = 0;
 }
 
 // acc += the products of a block whose codes are b.  fragment(m, j) gives A's fragment m of step j, in decode's
@@ -316,21 +340,21 @@ __device__ __forceinline__ void w4_exact_fragment(const W4Params& p, const Ragge
   const int lane = threadIdx.x & 63, quarter = lane >> 4;
   const GroupedParams& g = p.g;
   const uint8_t* const row = g.A + w4_row(p, t.row0 + min(r0 + (lane & 15), t.rows - 1)) * g.lda + quarter * 16;
-  const W4Columns<1> l = w4_columns<1>(p, t.group, n0, lane);
+  const W4Columns<1> l = w4_columns<G, 1>(p, t.group, n0, lane);
   f32x4_t acc[1][1];
   clear_sums(acc);
   const int whole = g.K / kW4Block, left = g.K % kW4Block / 32;
 #pragma unroll 1
   for (int c = 0; c < whole + (left > 0); ++c) {
     const int steps = c < whole ? 4 : left;
-    W4Weights<G, 1> k;
+    W4Weights<1> k;
     W4Rows x;
-    load_weights<false, ZEROS>(k, l, c, steps, quarter);
+    load_weights<false, ZEROS, G>(k, l, c, steps, quarter);
     load_rows<false>(x, row, c, steps);
-    end_weights(k, steps);
+    end_weights<G>(k, steps, quarter);
     block_products<IN, true, G>(acc, k.b, [&](int, int j) __attribute__((always_inline)) {
       return order_a<IN>(x.a[j]);
-    }, scales_of<IN, ZEROS>(k));
+    }, W4Scales<IN, ZEROS, G, 1>(k));
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -341,7 +365,7 @@ __device__ __forceinline__ void w4_exact_fragment(const W4Params& p, const Ragge
 
 // ---- the waves split K ---------------------------------------------------------------------------
 
-constexpr int kW4Waves = 4;
+constexpr int kW4Waves = 4;  // eight: 1 × 14336 × 4096 11.6 µs for 10.1, 33 × 2049 × 8160 14.7 for 14.3
 
 // For few tiles: a workgroup owns 16 rows and 16·FN columns, and its waves split K; everything goes straight from
 // memory to registers, a block ahead of the products.
@@ -354,23 +378,23 @@ __global__ void __launch_bounds__(64 * kW4Waves, 2) gemm_w4_kernel(W4Params p) {
   RaggedTile t;
   if (!w4_tile<16>(g, t)) return;
   const int n0 = t.tn * 16 * FN;
-  const W4Columns<FN> l = w4_columns<FN>(p, t.group, n0, lane);
+  const W4Columns<FN> l = w4_columns<G, FN>(p, t.group, n0, lane);
   const uint8_t* const row = g.A + w4_row(p, t.row0 + min(lane & 15, t.rows - 1)) * g.lda + quarter * 16;
   // The wave's share of K: consecutive blocks (a cache line of codes holds two).
   const int whole = g.K / kW4Block, left = g.K % kW4Block / 32;
   const int first = (int)((uint32_t)whole * wave / W), end = (int)((uint32_t)whole * (wave + 1) / W);
   f32x4_t acc[1][FN];
   clear_sums(acc);
-  W4Weights<G, FN> k0, k1;
+  W4Weights<FN> k0, k1;
   W4Rows x0, x1;
-  auto load = [&](W4Weights<G, FN>& k, W4Rows& x, int c) __attribute__((always_inline)) {
-    load_weights<true, ZEROS>(k, l, c, 4, quarter);
+  auto load = [&](W4Weights<FN>& k, W4Rows& x, int c) __attribute__((always_inline)) {
+    load_weights<true, ZEROS, G>(k, l, c, 4, quarter);
     load_rows<true>(x, row, c, 4);
   };
-  auto products = [&](W4Weights<G, FN>& k, const W4Rows& x) __attribute__((always_inline)) {
+  auto products = [&](W4Weights<FN>& k, const W4Rows& x) __attribute__((always_inline)) {
     block_products<IN, false, G>(acc, k.b, [&](int, int j) __attribute__((always_inline)) {
       return order_a<IN>(x.a[j]);
-    }, scales_of<IN, ZEROS>(k));
+    }, W4Scales<IN, ZEROS, G, FN>(k));
   };
   if (first < end) {
     // Every load of the loop is issued on every path (past the end the last block again): the waits before the
@@ -386,9 +410,9 @@ __global__ void __launch_bounds__(64 * kW4Waves, 2) gemm_w4_kernel(W4Params p) {
     if (c < end) products(k0, x0);
   }
   if (left > 0 && wave == W - 1) {
-    load_weights<false, ZEROS>(k0, l, whole, left, quarter);
+    load_weights<false, ZEROS, G>(k0, l, whole, left, quarter);
     load_rows<false>(x0, row, whole, left);
-    end_weights(k0, left);
+    end_weights<G>(k0, left, quarter);
     products(k0, x0);
   }
 #pragma unroll
@@ -508,7 +532,7 @@ __global__ void __launch_bounds__(256, PER) gemm_w4_panel_kernel(W4Params p) {
     }
   };
 
-  const W4Columns<FN> l = w4_columns<FN>(p, t.group, min(n0, g.N - 1), lane);
+  const W4Columns<FN> l = w4_columns<G, FN>(p, t.group, min(n0, g.N - 1), lane);
   u32x4_t b[D][FN];
   auto load_b = [&](int d, int c) __attribute__((always_inline)) {
     c = min(c, last);

@@ -179,18 +179,18 @@ inline TileChoice choose_mx4(int64_t groups, int64_t M, int64_t N, int64_t K, in
 }
 
 // Rows times weights in 4-bit codes (gemm_w4.hpp), dense (groups == 0) or ragged.  The panel kernel (128 columns
-// and 16, 32 or 64 rows a workgroup, A in LDS) needs a workgroup for most of the CUs; below that the waves of a
-// workgroup of 16 rows split K, over as many columns (64, 32, 16) as leave most of the CUs a workgroup.  µs, K = 4096,
-// group 128, bf16, by rows × columns; split K with 16, 32, 64 columns, then panels of 16, 32, 64 rows:
-//     1 ×  4096    5.1   6.2   8.4   19.4  24.2  34.2        64 ×  4096   23.3  15.9  12.4   20.1  25.3  35.6
-//     1 × 14336   12.3  10.5  10.2   19.8  25.3  35.0        64 × 14336   73.6  46.3  37.0   26.6  25.9  36.0
-//    16 × 14336   23.7  16.3  13.1   20.3  25.3  35.5       256 ×  4096   82.3  51.4  37.0   26.3  25.8  35.8
-//    32 × 14336   39.6  28.4  20.9   20.7  25.6  35.7       256 × 14336    280   172   118   80.2  66.0  55.9
+// and 16, 32 or 64 rows a workgroup, A in LDS) needs a workgroup for every CU; below that the waves of a workgroup of
+// 16 rows split K, over as many columns (64, 32, 16) as leave most of the CUs a workgroup.  µs, K = 4096, group 128,
+// bf16, by rows × columns; split K with 16, 32, 64 columns, then panels of 16, 32, 64 rows:
+//     1 ×  4096    5.0   6.0   8.2   19.4  24.4  34.2        64 ×  4096   23.7  16.1  12.6   20.3  25.7  35.6
+//     1 × 14336   12.2  10.6  10.1   19.8  25.0  35.0        64 ×  8192   44.0  27.9  20.9   20.7  25.4  36.0
+//    16 × 14336   24.0  16.4  12.9   20.2  25.5  35.5        64 × 14336   74.3  46.3  37.2   26.8  26.4  36.0
+//    32 × 14336   38.6  28.1  20.9   20.8  25.8  35.7       256 ×  4096   82.3  51.4  37.0   26.3  25.8  35.8
+//   (group 32,    39.5  28.9  22.6   27.5  32.4             256 × 14336    280   172   118   80.2  66.0  55.9
+//    with zeros)
 // 64 groups, 64 rows (8 of 64 experts for 8 tokens), N = 4096, K = 2048: 64.3, 50.6, 46.7; 41.7, 48.5, 76.6;
 // 2008 rows, N = 2048, K = 4096, group 64 with zeros: 393, 250, 184; 143, 135, 163.
-// Split K over 64 columns is not built for groups of 32 with zeros, whose scales and zeros do not fit the registers
-// (`wide` false; 16 × 14336: 25.4, 18.3 and, spilled, 23.1).
-inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, bool wide, int cus) {
+inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, int cus) {
   TileChoice c{};
   const double active = groups > 0 ? (double)(groups < M ? groups : M) : 1.0, rows = (double)M / active;
   auto tiles = [&](int bm, int bn) {  // ragged groups of the average size, each ending half way into its last tile
@@ -198,10 +198,10 @@ inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, bool wide, int
     return active * (per > 1 ? per : 1) * (double)tile_count(N, bn);
   };
   const double most = 0.75 * cus;
-  c.few = tiles(16, 128) < most;
+  c.few = tiles(16, 128) < cus;
   if (c.few) {
     c.bm = 16;
-    c.bn = wide && tiles(16, 64) >= most ? 64 : tiles(16, 32) >= most ? 32 : 16;
+    c.bn = tiles(16, 64) >= most ? 64 : tiles(16, 32) >= most ? 32 : 16;
   } else {
     c.bm = rows > 32 && tiles(64, 128) >= most ? 64 : rows > 16 && tiles(32, 128) >= most ? 32 : 16;
     c.bn = 128;
