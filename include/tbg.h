@@ -575,8 +575,8 @@ tbg_status tbg_expert_sort(int64_t slots, int64_t groups, const int32_t* experts
 /* out[place[t*top_k + j]] <- X[t] for every choice j of every token t: the rows of the groups.
  *   X         tokens rows of cols elements (any type: they are copied), ldx >= cols.
  *   place     int32, tokens*top_k values, as tbg_expert_sort gives them.  Values outside 0..rows-1 are no
- *             row.  Rows that no slot holds are left as they were; of slots that hold the same row
- *             (tbg_expert_sort makes none) either one's token is written.
+ *             row.  Rows that no slot holds are left as they were; where slots hold the same row
+ *             (tbg_expert_sort makes none) each of its elements is one of their tokens'.
  *   out       rows rows of the same type, ld_out >= cols; must not overlap X or place.
  * Any alignment of whole elements.  Codes and scales of microscaled 4-bit rows are matrices of TBG_U8.
  * The gradient of X is tbg_expert_combine of out's without weights.
@@ -603,7 +603,8 @@ tbg_status tbg_expert_combine(int64_t tokens, int64_t top_k, int64_t rows, int64
 
 /* The gradients of Y and of the weights under tbg_expert_combine, dout being the gradient of its out:
  *   dY[place[s]]   <- weights[s] * dout[t], rounded once to Y's type.  Rows that no slot holds are left as
- *                     they were.
+ *                     they were; where slots hold the same row (tbg_expert_sort makes none) nothing is
+ *                     added up: each of its elements is that of one of them.
  *   dweights[s]    <- the sum over the columns of Y[place[s]] * dout[t], held in fp32; 0 for a slot without
  *                     a row.
  *   dout           tokens rows, TBG_F32 or Y's type, ldd >= cols.
@@ -626,7 +627,7 @@ tbg_status tbg_expert_combine_grad(int64_t tokens, int64_t top_k, int64_t rows, 
  *   zeros     one byte each, K/group rows of N, ld_z bytes apart; NULL: every zero is 8. */
 
 /* C <- alpha·A·Wᵀ + beta·C for M rows of activations A (TBG_BF16 or TBG_F16, lda >= K, any alignment of whole
- * elements) and a weight matrix as above; C TBG_F32 or A's type, ldc >= N.
+ * elements) and a weight matrix as above; C TBG_F32 or A's type, ldc >= N; it must not overlap the inputs.
  * Per group the sum of A times whole numbers is held in fp32, multiplied by the scale and added in fp32;
  * nothing else is rounded before C, once, to nearest even.  alpha, beta as tbg_gemm_ex.  Made for few rows
  * (the bytes of W are the cost); any number is taken.

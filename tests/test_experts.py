@@ -307,6 +307,27 @@ def test_rows_outside_are_no_rows():
     assert torch.equal(dw.flatten(), want)  # whole numbers below 2^24
 
 
+@gpu
+@pytest.mark.parametrize("top_k,cols", [(2, 5), (4, 20), (9, 1501)])
+def test_slots_that_hold_the_same_row(top_k, cols):
+    """Of slots that hold one row, every element is one of theirs; combine and dweights count each slot."""
+    ops = _ops()
+    tokens = 6
+    x = torch.randint(1, 9, (tokens, cols), generator=_gen(3), device="cuda").float()
+    place = (torch.arange(tokens * top_k, dtype=torch.int32, device="cuda") % 4).reshape(tokens, top_k).contiguous()
+    w = torch.randint(1, 9, (tokens, top_k), generator=_gen(4), device="cuda").float()
+    out = ops.expert_dispatch(x, place, out=torch.full((5, cols), -1.0, device="cuda"))
+    dy, dw = ops.expert_combine_grad(x, out, place, w, dy=torch.full((5, cols), -1.0, device="cuda"))
+    for row in range(4):
+        t, j = (place == row).nonzero(as_tuple=True)
+        assert bool((out[row] == x[t]).any(dim=0).all())
+        assert bool((dy[row] == w[t, j, None] * x[t]).any(dim=0).all())
+    assert bool((out[4] == -1).all()) and bool((dy[4] == -1).all())
+    # whole numbers: at most 1501 * 64 and 9 * 64, which fp32 holds
+    assert torch.equal(dw, (out[place.long()] * x[:, None]).sum(-1))
+    assert torch.equal(ops.expert_combine(out, place, w), (w[..., None] * out[place.long()]).sum(1))
+
+
 # ---- rows back to their tokens ----------------------------------------------------------------------
 
 def _combine64(y, place, w):

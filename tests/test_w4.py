@@ -115,6 +115,21 @@ def test_no_ops_need_no_device():
     tbg.w4_gemm_grouped(**_grouped_args(M=0))
 
 
+def test_unused_pitches_do_not_limit_columns():
+    """alpha 0 leaves A and W out, their pitches with them: N past the limit of a pitch of codes is taken."""
+    N = (1 << 23) + 32
+    tbg.w4_gemm(**_args(M=0, N=N, alpha=0.0, lda=0, ldb=0, ld_s=0, ld_z=0, ldc=N))
+
+
+@gpu
+def test_alpha_zero_of_many_columns():
+    N = (1 << 23) + 17
+    c = torch.ones(N, device="cuda")
+    tbg.w4_gemm(**_args(M=1, N=N, alpha=0.0, A=0, codes=0, scales=0, zeros=0, beta=2.0, C=c.data_ptr(), ldc=N,
+                        c_dtype="f32"), stream=torch.cuda.current_stream().cuda_stream)
+    assert bool((c == 2).all())
+
+
 def test_helpers_refuse_host_tensors():
     a, c, s = torch.zeros((2, 64)).half(), torch.zeros((8, 32), dtype=torch.uint8), torch.zeros((2, 8)).half()
     with pytest.raises(ValueError):

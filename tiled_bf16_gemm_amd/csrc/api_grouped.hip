@@ -492,7 +492,8 @@ tbg_status w4_gemm_impl(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t
   if (alpha == 0.f) {  // nothing of A or W is used
     K = 0;
     A = codes = scales = zeros = nullptr;
-    lda = ldb = ld_s = ld_z = stride_b = stride_s = stride_z = N > 0 ? round_up(N, 16) : 16;
+    lda = ldb = stride_b = 16;
+    ld_s = ld_z = stride_s = stride_z = N > 0 ? N : 1;
   }
   st = check_ld("lda", lda, K, kMaxLdc);
   if (st == TBG_OK) st = check_ld("ldb", ldb, K / 2, kMaxPitch4);
