@@ -554,8 +554,8 @@ tbg_status tbg_mx4_gemm_grouped(int64_t groups, int64_t M, int64_t N, int64_t K,
  * rows of the groups; `place` says which row a slot became, `source` which slot a row came from.  All of
  * it is device memory read when the work runs, so a captured graph replays with new choices. */
 
-/* Workspace bytes tbg_expert_sort needs: 0 up to 4096 slots, above that the counts of up to 256 parts of
- * the slots by expert.  0 for sizes the call refuses. */
+/* Workspace bytes tbg_expert_sort needs: 0 for few slots (4096 up to 512 groups, 512 at 4096 groups), above that
+ * the counts of up to 256 parts of the slots by expert.  0 for sizes the call refuses. */
 size_t tbg_expert_sort_workspace_query(int64_t slots, int64_t groups);
 
 /* A stable sort of the slots by expert.

@@ -10,6 +10,10 @@
 // row; the last unit of a row is moved back to end with the row, so that rows of any length take only
 // whole 16-byte accesses (the bytes that two units share get the same values from both).  Rows shorter
 // than that go element by element.
+//
+// Bound by memory: 8192 tokens of 8 KiB, dispatch to 2 rows each 38 µs (5.3 TB/s), combine of 8 rows each
+// 103 µs (5.9), combine_grad of 2 rows each 52 µs (6.5, part of it from the cache).  Few tokens are a launch:
+// combine of 8 tokens, 8 rows each, 3.7 µs.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -182,14 +182,14 @@ inline TileChoice choose_mx4(int64_t groups, int64_t M, int64_t N, int64_t K, in
 // and 16, 32 or 64 rows a workgroup, A in LDS) needs a workgroup for every CU; below that the waves of a workgroup of
 // 16 rows split K, over as many columns (64, 32, 16) as leave most of the CUs a workgroup.  µs, K = 4096, group 128,
 // bf16, by rows × columns; split K with 16, 32, 64 columns, then panels of 16, 32, 64 rows:
-//     1 ×  4096    5.0   6.0   8.2   19.4  24.4  34.2        64 ×  4096   23.7  16.1  12.6   20.3  25.7  35.6
-//     1 × 14336   12.2  10.6  10.1   19.8  25.0  35.0        64 ×  8192   44.0  27.9  20.9   20.7  25.4  36.0
-//    16 × 14336   24.0  16.4  12.9   20.2  25.5  35.5        64 × 14336   74.3  46.3  37.2   26.8  26.4  36.0
-//    32 × 14336   38.6  28.1  20.9   20.8  25.8  35.7       256 ×  4096   82.3  51.4  37.0   26.3  25.8  35.8
-//   (group 32,    39.5  28.9  22.6   27.5  32.4             256 × 14336    280   172   118   80.2  66.0  55.9
+//     1 ×  4096    5.1   6.1   8.4   19.6  24.3  34.3        64 ×  4096   23.5  16.4  12.7   20.7  25.6  35.8
+//     1 × 14336   12.6  10.6  10.0   19.8  25.0  35.1        64 ×  8192   44.3  28.4  21.0   20.9  25.6  36.2
+//    16 × 14336   23.4  16.4  12.9   20.2  25.4  35.4        64 × 14336   74.3  46.9  37.1   26.7  26.1  36.1
+//    32 × 14336   38.4  28.0  20.7   20.9  25.8  35.6       256 ×  4096   83.2  52.1  37.0   26.8  26.0  35.8
+//   (group 32,    41.2  29.6  22.8   27.4  32.4  47.6       256 × 14336    281   172   118   79.3  63.2  54.6
 //    with zeros)
-// 64 groups, 64 rows (8 of 64 experts for 8 tokens), N = 4096, K = 2048: 64.3, 50.6, 46.7; 41.7, 48.5, 76.6;
-// 2008 rows, N = 2048, K = 4096, group 64 with zeros: 393, 250, 184; 143, 135, 163.
+// 64 groups, 64 rows (8 of 64 experts for 8 tokens), N = 4096, K = 2048: 66.3, 50.8, 46.4; 41.5, 49.7, 77.2;
+// 2008 rows, N = 2048, K = 4096, group 64 with zeros: 383, 241, 175; 143, 135, 158.
 inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, int cus) {
   TileChoice c{};
   const double active = groups > 0 ? (double)(groups < M ? groups : M) : 1.0, rows = (double)M / active;
