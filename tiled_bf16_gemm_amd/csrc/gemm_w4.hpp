@@ -57,21 +57,44 @@ __device__ __forceinline__ bf16x8_t order_a(const u32x4_t& a) {
 
 typedef _Float16 f16x2v_t __attribute__((ext_vector_type(2)));
 
-// The eight codes of a dword as values: fp16 c - z; bf16 c, or with EXACT c - z.
+// A zero as decode wants it: bf16 a float; fp16 -1024 - z in the upper half (z is below the last place of 1024, so its
+// bits are those of -1024 and z's).
+template <int IN>
+__device__ __forceinline__ uint32_t zero_word(uint32_t z) {
+  return IN == 1 ? z << 16 | 0xE4000000u : __float_as_uint((float)z);
+}
+
+// What decode's masks are held in: an instruction takes one constant from a scalar register, so (w & m) | o is a single
+// one only where o is in a vector register.  (Left to the compiler they are two with a literal each.)
+template <int IN>
+struct W4Masks {
+  uint32_t low = 0x000F000Fu, high = 0x00F000F0u, bits = 0x64006400u;
+  __device__ __forceinline__ W4Masks() {
+    if constexpr (IN == 1) {
+      asm("" : "+s"(low));
+      asm("" : "+s"(high));
+      asm("" : "+v"(bits));
+    }
+  }
+};
+
+// The eight codes of a dword as values: fp16 c - z; bf16 c, or with EXACT c - z.  z: zero_word.
 template <int IN, bool EXACT>
-__device__ __forceinline__ bf16x8_t decode(uint32_t w, float z) {
+__device__ __forceinline__ bf16x8_t decode(uint32_t w, uint32_t z, const W4Masks<IN>& m) {
   u32x4_t r;
   if constexpr (IN == 1) {
-    const _Float16 one = (_Float16)(-1024.f - z), sixteen = (_Float16)(-64.f - z);
+    const _Float16 one = __builtin_bit_cast(f16x2v_t, z)[1], sixteen = one + (_Float16)960.f;  // -64 - z, exactly
     const f16x2v_t off1 = {one, one}, off16 = {sixteen, sixteen}, part = {(_Float16)0.0625f, (_Float16)0.0625f};
     const uint32_t v = w >> 8;
-    auto pair = [](uint32_t x, uint32_t mask) { return __builtin_bit_cast(f16x2v_t, (x & mask) | 0x64006400u); };
-    r[0] = __builtin_bit_cast(uint32_t, pair(w, 0x000F000Fu) + off1);
-    r[1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(pair(w, 0x00F000F0u), part, off16));
-    r[2] = __builtin_bit_cast(uint32_t, pair(v, 0x000F000Fu) + off1);
-    r[3] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(pair(v, 0x00F000F0u), part, off16));
+    auto pair = [&](uint32_t x, uint32_t mask) { return __builtin_bit_cast(f16x2v_t, (x & mask) | m.bits); };
+    r[0] = __builtin_bit_cast(uint32_t, pair(w, m.low) + off1);
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(pair(w, m.high), part, off16));
+    r[2] = __builtin_bit_cast(uint32_t, pair(v, m.low) + off1);
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(pair(v, m.high), part, off16));
   } else if constexpr (EXACT) {
-    auto value = [&](int i) { return __float_as_uint((float)((w >> (4 * i)) & 15u) - z); };  // whole: its low half is 0
+    auto value = [&](int i) {  // whole: its low half is 0
+      return __float_as_uint((float)((w >> (4 * i)) & 15u) - __uint_as_float(z));
+    };
     r[0] = high_halves(value(0), value(2));
     r[1] = high_halves(value(4), value(6));
     r[2] = high_halves(value(1), value(3));
@@ -193,9 +216,10 @@ __device__ __forceinline__ float scale_value(uint16_t s) {
   return __uint_as_float((uint32_t)s << 16);
 }
 
-// A group's scale and zero for a lane's column.
+// A group's scale and zero (zero_word) for a lane's column.
 struct W4Scale {
-  float s, z;
+  float s;
+  uint32_t z;
 };
 
 // The groups' scales and zeros for every quarter, from the quarters that hold them: a scale and a zero are one dword,
@@ -210,7 +234,7 @@ struct W4Scales {
 #pragma unroll
     for (int n = 0; n < FN; ++n) {
       uint32_t r[4];
-      r[0] = k.s[n] | (ZEROS ? (uint32_t)k.z[n] << 16 : 0u);
+      r[0] = k.s[n] | (ZEROS ? (uint32_t)k.z[n] << 16 : 0u) | (IN == 1 && ZEROS ? 0xE4000000u : 0u);
       if (G == 32) {  // rows 0 0 2 2 and 1 1 3 3
         r[1] = r[0];
         swap_rows(r[0], r[1]);
@@ -226,7 +250,8 @@ struct W4Scales {
     }
   }
   __device__ __forceinline__ W4Scale operator()(int g, int n) const {
-    return W4Scale{scale_value<IN>((uint16_t)v[g][n]), ZEROS ? (float)(v[g][n] >> 16) : 8.f};
+    const uint32_t x = v[g][n];
+    return W4Scale{scale_value<IN>((uint16_t)x), !ZEROS ? zero_word<IN>(8) : IN == 1 ? x : zero_word<IN>(x >> 16)};
   }
 };
 
@@ -248,6 +273,7 @@ __device__ __forceinline__ void block_products(f32x4_t (&acc)[FM][FN], u32x4_t (
   for (int n = 0; n < FN; ++n) turn_quarters(b[n]);
   f32x4_t sum[FM][FN], of_a[FM];
   W4Scale sz[FN];
+  const W4Masks<IN> masks;
   bf16x8_t a[2][FM];
 #pragma unroll
   for (int m = 0; m < FM; ++m) a[0][m] = fragment(m, 0);
@@ -274,7 +300,7 @@ __device__ __forceinline__ void block_products(f32x4_t (&acc)[FM][FN], u32x4_t (
     }
 #pragma unroll
     for (int n = 0; n < FN; ++n) {
-      const bf16x8_t v = decode<IN, EXACT>(b[n][j], sz[n].z);
+      const bf16x8_t v = decode<IN, EXACT>(b[n][j], sz[n].z, masks);
 #pragma unroll
       for (int m = 0; m < FM; ++m) mfma16<false, IN>(sum[m][n], a[j & 1][m], v);
     }
@@ -285,7 +311,7 @@ __device__ __forceinline__ void block_products(f32x4_t (&acc)[FM][FN], u32x4_t (
         for (int m = 0; m < FM; ++m)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float x = Sums ? fmaf(-sz[n].z, of_a[m][i], sum[m][n][i]) : sum[m][n][i];
+            const float x = Sums ? fmaf(-__uint_as_float(sz[n].z), of_a[m][i], sum[m][n][i]) : sum[m][n][i];
             acc[m][n][i] = fmaf(sz[n].s, x, acc[m][n][i]);
           }
       // The sums are used up here: moved into a later block of the code they would stay in registers until there.
@@ -533,7 +559,7 @@ __global__ void __launch_bounds__(256, PER) gemm_w4_panel_kernel(W4Params p) {
       const int i = threadIdx.x + 256 * e;
       float s = scale_value<IN>(s_next[slot][e]);
       if (left > 0 && c >= last && i / Columns * (G / 32) >= left) s = 0.f;
-      if (Pairs % 256 == 0 || i < Pairs) pair[c & 1][i] = W4Scale{s, ZEROS ? (float)z_next[slot][e] : 8.f};
+      if (Pairs % 256 == 0 || i < Pairs) pair[c & 1][i] = W4Scale{s, zero_word<IN>(ZEROS ? z_next[slot][e] : 8)};
     }
   };
 
