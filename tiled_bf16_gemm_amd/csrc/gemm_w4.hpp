@@ -28,7 +28,7 @@
 // blocks in LDS.  Rows and columns past the end repeat the last one and are not stored.  choose_w4
 // (tile_choice.hpp) has both sides' figures.
 //
-// Measured: 1 × 14336 × 4096 9.3 µs (30 MB, 3.3 TB/s: the latency of 8 blocks a wave after the launch); 64 rows over 40 of
+// Measured: 1 × 14336 × 4096 9.3 µs (30 MB, 3.3 TB/s: 8 blocks in a row a wave after the launch); 64 rows over 40 of
 // 64 experts of 4096 × 2048 41 µs (173 MB, 4.2 TB/s); 2008 rows over 64 of 2048 × 4096 121-127 µs, where vector
 // instructions issue in 71 % of the busy cycles and products in 34 %.  Taking z off with products against -z in the same
 // sum (152 vector instructions a block for 164, 32 products for 24) was 3 to 8 % slower there.
@@ -224,7 +224,7 @@ struct W4Scale {
 
 // The groups' scales and zeros for every quarter, from the quarters that hold them: a scale and a zero are one dword,
 // whose rows of 16 lanes are copied to the others with the swaps of turn_quarters.  (A load for every group and column
-// would be 16 of 22 loads a block for groups of 32 with zeros and two fragments: 33 × 2049 × 8160 16.2 µs, so 13.0.)
+// would be 16 of 22 loads a block for groups of 32 with zeros and two fragments: 33 × 2049 × 8160 16.2 µs, so 13.0; with the masks of W4Masks 12.5.)
 template <int IN, bool ZEROS, int G, int FN>
 struct W4Scales {
   static constexpr int Groups = kW4Block / G;
