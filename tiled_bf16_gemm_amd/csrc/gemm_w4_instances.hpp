@@ -11,8 +11,8 @@ static hipError_t launch_w4_tile(const W4Params& p, const TileChoice& c, hipStre
   if (c.few && c.bn == 16) hipLaunchKernelGGL((gemm_w4_kernel<IN, ZEROS, G, 1>), g, t, 0, s, p);
   else if (c.few && c.bn == 32) hipLaunchKernelGGL((gemm_w4_kernel<IN, ZEROS, G, 2>), g, t, 0, s, p);
   else if (c.few) hipLaunchKernelGGL((gemm_w4_kernel<IN, ZEROS, G, 4>), g, t, 0, s, p);
-  else if (c.bm == 16) hipLaunchKernelGGL((gemm_w4_panel_kernel<IN, ZEROS, G, 1, 2, 3>), g, t, 0, s, p);
-  else if (c.bm == 32) hipLaunchKernelGGL((gemm_w4_panel_kernel<IN, ZEROS, G, 2, 2, 2>), g, t, 0, s, p);
+  else if (c.bm == 16) hipLaunchKernelGGL((gemm_w4_panel_kernel<IN, ZEROS, G, 1, 2, 5>), g, t, 0, s, p);
+  else if (c.bm == 32) hipLaunchKernelGGL((gemm_w4_panel_kernel<IN, ZEROS, G, 2, 2, 4>), g, t, 0, s, p);
   else hipLaunchKernelGGL((gemm_w4_panel_kernel<IN, ZEROS, G, 4, 2, 2>), g, t, 0, s, p);
   return hipGetLastError();
 }
