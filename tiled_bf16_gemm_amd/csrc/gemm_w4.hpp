@@ -29,8 +29,8 @@
 // (tile_choice.hpp) has both sides' figures.
 //
 // Measured: 1 × 14336 × 4096 9.3 µs (30 MB, 3.3 TB/s: 8 blocks in a row a wave after the launch); 64 rows over 40 of
-// 64 experts of 4096 × 2048 41 µs (173 MB, 4.2 TB/s); 2008 rows over 64 of 2048 × 4096 121-127 µs, where vector
-// instructions issue in 71 % of the busy cycles and products in 34 %.  Taking z off with products against -z in the same
+// 64 experts of 4096 × 2048 39.5 µs (173 MB, 4.4 TB/s); 2008 rows over 64 of 2048 × 4096 118-127 µs, where vector
+// instructions issue in 77 % of the busy cycles and products in 37 %.  Taking z off with products against -z in the same
 // sum (152 vector instructions a block for 164, 32 products for 24) was 3 to 8 % slower there.
 #pragma once
 #include "gemm_common.hpp"

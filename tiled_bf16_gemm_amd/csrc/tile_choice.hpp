@@ -182,14 +182,14 @@ inline TileChoice choose_mx4(int64_t groups, int64_t M, int64_t N, int64_t K, in
 // and 16, 32 or 64 rows a workgroup, A in LDS) needs a workgroup for every CU; below that the waves of a workgroup of
 // 16 rows split K, over as many columns (64, 32, 16) as leave most of the CUs a workgroup.  µs, K = 4096, group 128,
 // bf16, by rows × columns; split K with 16, 32, 64 columns, then panels of 16, 32, 64 rows:
-//     1 ×  4096    5.1   6.1   8.4   19.6  24.3  34.3        64 ×  4096   23.5  16.4  12.7   20.7  25.6  35.8
-//     1 × 14336   12.6  10.6  10.0   19.8  25.0  35.1        64 ×  8192   44.3  28.4  21.0   20.9  25.6  36.2
-//    16 × 14336   23.4  16.4  12.9   20.2  25.4  35.4        64 × 14336   74.3  46.9  37.1   26.7  26.1  36.1
-//    32 × 14336   38.4  28.0  20.7   20.9  25.8  35.6       256 ×  4096   83.2  52.1  37.0   26.8  26.0  35.8
-//   (group 32,    41.2  29.6  22.8   27.4  32.4  47.6       256 × 14336    281   172   118   79.3  63.2  54.6
+//     1 ×  4096    5.1   6.1   8.3   17.9  23.0  34.1        64 ×  4096   23.6  16.3  12.4   19.0  24.3  36.2
+//     1 × 14336   12.5  10.6  10.0   18.7  23.8  35.0        64 ×  8192   44.0  28.5  21.2   19.5  24.4  36.1
+//    16 × 14336   23.4  16.4  12.8   19.0  23.9  35.3        64 × 14336   75.9  47.8  37.6   26.1  24.6  36.0
+//    32 × 14336   39.5  28.5  21.0   19.4  24.4  36.0       256 ×  4096   84.2  52.2  36.9   25.8  24.6  35.7
+//   (group 32,    40.8  29.6  23.0   28.6  31.8  47.1       256 × 14336    281   172   118   79.2  59.6  54.9
 //    with zeros)
-// 64 groups, 64 rows (8 of 64 experts for 8 tokens), N = 4096, K = 2048: 66.3, 50.8, 46.4; 41.5, 49.7, 77.2;
-// 2008 rows, N = 2048, K = 4096, group 64 with zeros: 383, 241, 175; 143, 135, 158.
+// 64 groups, 64 rows (8 of 64 experts for 8 tokens), N = 4096, K = 2048: 64.6, 51.0, 47.9; 40.5, 49.2, 73.7;
+// 2008 rows, N = 2048, K = 4096, group 64 with zeros: 383, 240, 176; 140, 127, 160.
 inline TileChoice choose_w4(int64_t groups, int64_t M, int64_t N, int cus) {
   TileChoice c{};
   const double active = groups > 0 ? (double)(groups < M ? groups : M) : 1.0, rows = (double)M / active;
