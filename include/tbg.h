@@ -630,7 +630,8 @@ tbg_status tbg_expert_combine_grad(int64_t tokens, int64_t top_k, int64_t rows, 
  * elements) and a weight matrix as above; C TBG_F32 or A's type, ldc >= N; it must not overlap the inputs.
  * Per group the sum of A times whole numbers is held in fp32, multiplied by the scale and added in fp32;
  * nothing else is rounded before C, once, to nearest even.  alpha, beta as tbg_gemm_ex.  Made for few rows
- * (the bytes of W are the cost); any number is taken.
+ * (the bytes of W are the cost); any number is taken.  For given sizes a row of C depends on its own row of A
+ * alone: an infinity or a NaN in another row leaves every bit of it as it is.
  * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.
  * Limits: M up to 2^30, ldb below 2^23 (K up to 2^24 - 32), ld_s and ld_z up to 2^28 (N too), workgroups as for the
  * ragged products.

@@ -525,3 +525,53 @@ def test_decoding_step_of_a_layer_of_experts():
             hh = (_weights(up[0][e], up[1][e], None) @ x[t].double()).clamp(-8, 8).round()
             want[t] += float(w[t, j]) * (_weights(down[0][e], down[1][e], None) @ hh)
     assert torch.equal(out.double(), want)
+
+
+# ---- rows beside one that is not finite -------------------------------------------------------------
+
+# every kernel and tile: K split over the waves with 16, 32 and 64 columns, panels of 16, 32 and 64 rows
+KERNELS = [(9, 400), (9, 7000), (9, 12400), (16, 32800), (30, 32800), (60, 32800)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_rows_keep_their_bits_beside_others_that_are_not_finite(M, N, dtype):
+    """A row's value, to the last bit, does not depend on what another row of its tile holds: a NaN or an infinity
+    there (another request's, a padding row's) leaves it as it is.  Real operands: another order of the sums shows."""
+    ops = _ops()
+    for K, G, zeros, out, beta in ((544, 32, True, "f32", 0.0), (256, 128, False, dtype, 0.0), (192, 64, True, "f32", -0.75)):
+        print(f"w4 {M}x{N}x{K} group {G} {dtype} beside a row that is not finite, beta {beta}", flush=True)
+        g = _gen(M + N + K)
+        code, s, z = _operands(g, (), N, K, G, dtype, zeros, False)
+        codes = _pack(code)
+        a = torch.randn((M, K), device="cuda", generator=g).to(TORCH[dtype])
+        old = torch.randn((M, N), device="cuda", generator=g).to(TORCH[out])
+        want = ops.w4_gemm(a, codes, s, z, out_dtype=out, out=old.clone(), beta=beta)
+        a[3, 17], a[5, 70], a[M - 1, K - 1] = float("inf"), float("nan"), float("-inf")
+        got = ops.w4_gemm(a, codes, s, z, out_dtype=out, out=old.clone(), beta=beta)
+        rest = [r for r in range(M) if r not in (3, 5, M - 1)]
+        assert torch.equal(got[rest], want[rest]), float((got[rest].double() - want[rest].double()).abs().max())
+        assert bool(torch.isfinite(want).all()) and not bool(torch.isfinite(got[[3, 5, M - 1]]).any())
+
+
+@gpu
+def test_rows_of_groups_keep_their_bits_beside_others_that_are_not_finite():
+    """The same over ragged groups, whose rows read A through source: also where a token that is not finite is the
+    last row of its group, which the rows past its end repeat."""
+    ops = _ops()
+    for sizes, N in (([5, 0, 1, 17, 9], 700), ([40, 33, 64, 1, 90], 7000)):
+        E, M, K, G = len(sizes), sum(sizes), 320, 64
+        g = _gen(N)
+        code, s, z = _operands(g, (E,), N, K, G, "bf16", True, False)
+        codes = _pack(code)
+        off = torch.tensor([0] + list(np.cumsum(sizes)), dtype=torch.int32, device="cuda")
+        a = torch.randn((M, K), device="cuda", generator=g).bfloat16()
+        source = torch.randperm(M, device="cuda", generator=g).to(torch.int32)
+        want = ops.w4_gemm_grouped(a, codes, s, off, z, source=source, out_dtype="f32")
+        bad = [0, sizes[0] - 1, M - 1]
+        a[source[bad].long(), 33] = float("inf")
+        got = ops.w4_gemm_grouped(a, codes, s, off, z, source=source, out_dtype="f32")
+        rest = [r for r in range(M) if r not in bad]
+        assert torch.equal(got[rest], want[rest])
+        assert bool(torch.isfinite(want).all()) and not bool(torch.isfinite(got[bad]).any())

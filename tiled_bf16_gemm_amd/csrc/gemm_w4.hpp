@@ -14,8 +14,8 @@
 //         a dword.  z is taken off after the group: sum a·(c - z) = sum a·c - z·(sum a), the sum of a being one
 //         more product, against ones, for all the columns of the wave.  Where a is infinite or near the
 //         end of its range that difference may not exist although the definition's sum does: a
-//         workgroup that meets a result which is not finite computes its tile again from c - z itself
-//         (28 instructions a dword).
+//         result that is not finite is computed again from c - z itself (28 instructions a dword), and
+//         it alone is stored from there, so that what a row holds never shows in another row's bits.
 //
 // Lane l holds column l%16 of a fragment and 16 bytes, the 32 codes of quarter l/16 of a block of 128.  The
 // product wants the four quarters of 32 codes side by side in a step, so that a step never crosses a group:
@@ -364,10 +364,18 @@ __device__ __forceinline__ void w4_store(const W4Params& p, int64_t row, int n, 
   else ((float*)g.C)[at] = x;
 }
 
-// The tile again, from c - z itself, for a result that is not finite: a wave takes one fragment of 16 rows and 16
-// columns after another over the whole of K and stores it.  Rarely taken, so it is kept small.
+// Whether the element that a lane holds i-th of the fragment of 16 rows and 16 columns at r0, n0 exists.
+__device__ __forceinline__ bool w4_in(const W4Params& p, const RaggedTile& t, int r0, int n0, int i) {
+  const int lane = threadIdx.x & 63;
+  return r0 + 4 * (lane >> 4) + i < t.rows && n0 + (lane & 15) < p.g.N;
+}
+
+// A fragment of 16 rows and 16 columns again, from c - z itself: a wave goes over the whole of K, and a lane stores
+// its element i where bit i of `again` is set (all of them exist), the results that were not finite.  The others
+// keep the sums they have: those of another order would depend on the tile's other rows.  Rarely taken, so it is
+// kept small.
 template <int IN, bool ZEROS, int G>
-__device__ __forceinline__ void w4_exact_fragment(const W4Params& p, const RaggedTile& t, int r0, int n0) {
+__device__ __forceinline__ void w4_exact_fragment(const W4Params& p, const RaggedTile& t, int r0, int n0, uint32_t again) {
   const int lane = threadIdx.x & 63, quarter = lane >> 4;
   const GroupedParams& g = p.g;
   const uint8_t* const row = g.A + w4_row(p, t.row0 + min(r0 + (lane & 15), t.rows - 1)) * g.lda + quarter * 16;
@@ -388,10 +396,8 @@ __device__ __forceinline__ void w4_exact_fragment(const W4Params& p, const Ragge
     }, W4Scales<IN, ZEROS, G, 1>(k));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 4 * quarter + i, n = n0 + (lane & 15);
-    if (r < t.rows && n < g.N) w4_store<IN>(p, t.row0 + r, n, acc[0][0][i]);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (again >> i & 1) w4_store<IN>(p, t.row0 + r0 + 4 * quarter + i, n0 + (lane & 15), acc[0][0][i]);
 }
 
 // ---- the waves split K ---------------------------------------------------------------------------
@@ -461,18 +467,27 @@ __global__ void __launch_bounds__(64 * kW4Waves, 2) gemm_w4_kernel(W4Params p) {
     for (int w = 0; w < W; ++w) x[i] += ((const float*)part[w])[at];
     finite = finite && is_finite(x[i]);
   }
-  if constexpr (IN == 0) {
-    if (__syncthreads_or(!finite)) {
-#pragma unroll 1
-      for (int n = wave; n < FN; n += W)
-        if (n0 + 16 * n < g.N) w4_exact_fragment<IN, ZEROS, G>(p, t, 0, n0 + 16 * n);
-      return;
-    }
-  }
+  const bool again = IN == 0 && __syncthreads_or(!finite);
 #pragma unroll
   for (int i = 0; i < FN; ++i) {
     const int e = threadIdx.x + 64 * W * i, r = e / (16 * FN), n = n0 + e % (16 * FN);
-    if (r < t.rows && n < g.N) w4_store<IN>(p, t.row0 + r, n, x[i]);
+    if (r < t.rows && n < g.N && (IN == 1 || is_finite(x[i]))) w4_store<IN>(p, t.row0 + r, n, x[i]);
+  }
+  if constexpr (IN == 0) {
+    if (again) {
+#pragma unroll 1
+      for (int n = wave; n < FN; n += W) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y = 0.f;  // x of the lane's elements of this fragment
+#pragma unroll
+          for (int w = 0; w < W; ++w) y += part[w][n][lane][i];
+          if (!is_finite(y) && w4_in(p, t, 0, n0 + 16 * n, i)) bad |= 1u << i;
+        }
+        if (__ballot(bad != 0) != 0) w4_exact_fragment<IN, ZEROS, G>(p, t, 0, n0 + 16 * n, bad);
+      }
+    }
   }
 }
 
@@ -608,21 +623,7 @@ __global__ void __launch_bounds__(256, PER) gemm_w4_panel_kernel(W4Params p) {
     for (int d = 0; d < D - 1; ++d)
       if (c + d < blocks) step(c + d, d);
   }
-  if constexpr (IN == 0) {
-    bool finite = true;
-#pragma unroll
-    for (int m = 0; m < FM; ++m)
-#pragma unroll
-      for (int n = 0; n < FN; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) finite = finite && is_finite(acc[m][n][i]);
-    if (__ballot(!finite) != 0) {  // the wave's own columns
-#pragma unroll 1
-      for (int f = 0; f < FM * FN; ++f)
-        if (n0 + f % FN * 16 < g.N) w4_exact_fragment<IN, ZEROS, G>(p, t, f / FN * 16, n0 + f % FN * 16);
-      return;
-    }
-  }
+  bool finite = true;
 #pragma unroll
   for (int m = 0; m < FM; ++m)
 #pragma unroll
@@ -630,8 +631,26 @@ __global__ void __launch_bounds__(256, PER) gemm_w4_panel_kernel(W4Params p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 16 * m + 4 * quarter + i, col = n0 + 16 * n + (lane & 15);
-        if (r < t.rows && col < g.N) w4_store<IN>(p, t.row0 + r, col, acc[m][n][i]);
+        const bool good = IN == 1 || is_finite(acc[m][n][i]);
+        if (r < t.rows && col < g.N && good) w4_store<IN>(p, t.row0 + r, col, acc[m][n][i]);
+        finite = finite && good;
       }
+  if constexpr (IN == 0) {
+    if (__ballot(!finite) != 0) {  // the wave's own columns
+      static_assert(4 * FM * FN <= 32, "a bit for every element of a lane");
+      uint32_t bad = 0;
+#pragma unroll
+      for (int f = 0; f < FM * FN; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!is_finite(acc[f / FN][f % FN][i]) && w4_in(p, t, f / FN * 16, n0 + f % FN * 16, i)) bad |= 1u << (4 * f + i);
+#pragma unroll 1
+      for (int f = 0; f < FM * FN; ++f) {
+        const uint32_t some = bad >> (4 * f) & 15u;
+        if (__ballot(some != 0) != 0) w4_exact_fragment<IN, ZEROS, G>(p, t, f / FN * 16, n0 + f % FN * 16, some);
+      }
+    }
+  }
 }
 
 }  // namespace tbg
