@@ -575,3 +575,30 @@ def test_rows_of_groups_keep_their_bits_beside_others_that_are_not_finite():
         rest = [r for r in range(M) if r not in bad]
         assert torch.equal(got[rest], want[rest])
         assert bool(torch.isfinite(want).all()) and not bool(torch.isfinite(got[bad]).any())
+
+
+@gpu
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_values_near_the_end_of_the_range(M, N):
+    """c·a passes fp32's range where (c - z)·a does not: such an element is the definition's sum, off by the bound of
+    a sum of a·(c - z) itself, whose terms with c = z are nothing at all; C's old value is read once for it."""
+    ops = _ops()
+    K, G, row, at, big = 544, 32, 6, 77, 1.5 * 2.0 ** 126
+    g = _gen(M + N)
+    code, s, z = _operands(g, (), N, K, G, "bf16", True, True)
+    z[at // G] = torch.randint(5, 15, (N,), device="cuda", generator=g, dtype=torch.uint8)  # c·a of c >= 4: above 2^128
+    d = torch.arange(N, device="cuda", dtype=torch.int32) % 3 - 1
+    code[:, at] = (z[at // G].int() + d).to(torch.uint8)
+    a = torch.randint(-4, 5, (M, K), device="cuda", generator=g).bfloat16()
+    a[row, at] = big
+    w = _weights(code, s, z)
+    old = torch.randint(-8, 9, (M, N), device="cuda", generator=g).float()
+    for beta in (0.0, 0.5):
+        exact = a.double() @ w.t().contiguous() + beta * old.double()
+        got = ops.w4_gemm(a, _pack(code), s, z, out_dtype="f32", out=old.clone(), beta=beta).double()
+        bound = (K + 3 * (K // G) + 16) * 2.0 ** -23 * (a[row].double().abs() @ w.abs().t().contiguous() + old[row].abs())
+        assert bool(((got[row] - exact[row]).abs() <= bound).all())
+        same = d == 0
+        assert int(same.sum()) > 100 and torch.equal(got[row][same], exact[row][same])  # whole quarters below 2^20
+        rest = [r for r in range(M) if r != row]
+        assert torch.equal(got[rest], exact[rest])
