@@ -364,40 +364,37 @@ __device__ __forceinline__ void w4_store(const W4Params& p, int64_t row, int n, 
   else ((float*)g.C)[at] = x;
 }
 
-// Whether the element that a lane holds i-th of the fragment of 16 rows and 16 columns at r0, n0 exists.
-__device__ __forceinline__ bool w4_in(const W4Params& p, const RaggedTile& t, int r0, int n0, int i) {
-  const int lane = threadIdx.x & 63;
-  return r0 + 4 * (lane >> 4) + i < t.rows && n0 + (lane & 15) < p.g.N;
-}
-
-// A fragment of 16 rows and 16 columns again, from c - z itself: a wave goes over the whole of K, and a lane stores
-// its element i where bit i of `again` is set (all of them exist), the results that were not finite.  The others
-// keep the sums they have: those of another order would depend on the tile's other rows.  Rarely taken, so it is
-// kept small.
+// Stores the fragment of 16 rows and 16 columns at r0, n0 of a tile with a result that is not finite; x: the lane's
+// sums.  Those that are not finite are computed again from c - z itself, by the wave over the whole of K; the others stay
+// as they are, as sums of another order would depend on the tile's other rows.  Rarely taken, so it is kept small.
 template <int IN, bool ZEROS, int G>
-__device__ __forceinline__ void w4_exact_fragment(const W4Params& p, const RaggedTile& t, int r0, int n0, uint32_t again) {
+__device__ __forceinline__ void w4_exact_fragment(const W4Params& p, const RaggedTile& t, int r0, int n0, const f32x4_t& x) {
   const int lane = threadIdx.x & 63, quarter = lane >> 4;
   const GroupedParams& g = p.g;
   const uint8_t* const row = g.A + w4_row(p, t.row0 + min(r0 + (lane & 15), t.rows - 1)) * g.lda + quarter * 16;
   const W4Columns<1> l = w4_columns<G, 1>(p, t.group, n0, lane);
   f32x4_t acc[1][1];
   clear_sums(acc);
+  const bool good = is_finite(x[0]) && is_finite(x[1]) && is_finite(x[2]) && is_finite(x[3]);
   const int whole = g.K / kW4Block, left = g.K % kW4Block / 32;
+  const int blocks = __ballot(!good) != 0 ? whole + (left > 0) : 0;
 #pragma unroll 1
-  for (int c = 0; c < whole + (left > 0); ++c) {
+  for (int c = 0; c < blocks; ++c) {
     const int steps = c < whole ? 4 : left;
     W4Weights<1> k;
-    W4Rows x;
+    W4Rows a;
     load_weights<false, ZEROS, G>(k, l, c, steps, quarter);
-    load_rows<false>(x, row, c, steps);
+    load_rows<false>(a, row, c, steps);
     end_weights<G>(k, steps, quarter);
     block_products<IN, true, G>(acc, k.b, [&](int, int j) __attribute__((always_inline)) {
-      return order_a<IN>(x.a[j]);
+      return order_a<IN>(a.a[j]);
     }, W4Scales<IN, ZEROS, G, 1>(k));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (again >> i & 1) w4_store<IN>(p, t.row0 + r0 + 4 * quarter + i, n0 + (lane & 15), acc[0][0][i]);
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * quarter + i, n = n0 + (lane & 15);
+    if (r < t.rows && n < g.N) w4_store<IN>(p, t.row0 + r, n, is_finite(x[i]) ? x[i] : acc[0][0][i]);
+  }
 }
 
 // ---- the waves split K ---------------------------------------------------------------------------
@@ -467,27 +464,24 @@ __global__ void __launch_bounds__(64 * kW4Waves, 2) gemm_w4_kernel(W4Params p) {
     for (int w = 0; w < W; ++w) x[i] += ((const float*)part[w])[at];
     finite = finite && is_finite(x[i]);
   }
-  const bool again = IN == 0 && __syncthreads_or(!finite);
+  if constexpr (IN == 0) {
+    if (__syncthreads_or(!finite)) {
+#pragma unroll 1
+      for (int n = wave; n < FN; n += W) {
+        f32x4_t y = {0.f, 0.f, 0.f, 0.f};  // x of the lane's elements of fragment n
+        int at = lane;  // (a value of its own: part's address, kept in a register from the stores above, made
+        asm volatile("" : "+v"(at));  // those wait for the loads past the end: 16 × 4096 × 4096 8.1 µs for 7.8)
+#pragma unroll
+        for (int w = 0; w < W; ++w) y += part[w][n][at];
+        if (n0 + 16 * n < g.N) w4_exact_fragment<IN, ZEROS, G>(p, t, 0, n0 + 16 * n, y);
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < FN; ++i) {
     const int e = threadIdx.x + 64 * W * i, r = e / (16 * FN), n = n0 + e % (16 * FN);
-    if (r < t.rows && n < g.N && (IN == 1 || is_finite(x[i]))) w4_store<IN>(p, t.row0 + r, n, x[i]);
-  }
-  if constexpr (IN == 0) {
-    if (again) {
-#pragma unroll 1
-      for (int n = wave; n < FN; n += W) {
-        uint32_t bad = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float y = 0.f;  // x of the lane's elements of this fragment
-#pragma unroll
-          for (int w = 0; w < W; ++w) y += part[w][n][lane][i];
-          if (!is_finite(y) && w4_in(p, t, 0, n0 + 16 * n, i)) bad |= 1u << i;
-        }
-        if (__ballot(bad != 0) != 0) w4_exact_fragment<IN, ZEROS, G>(p, t, 0, n0 + 16 * n, bad);
-      }
-    }
+    if (r < t.rows && n < g.N) w4_store<IN>(p, t.row0 + r, n, x[i]);
   }
 }
 
@@ -623,7 +617,26 @@ __global__ void __launch_bounds__(256, PER) gemm_w4_panel_kernel(W4Params p) {
     for (int d = 0; d < D - 1; ++d)
       if (c + d < blocks) step(c + d, d);
   }
-  bool finite = true;
+  if constexpr (IN == 0) {
+    bool finite = true;
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) finite = finite && is_finite(acc[m][n][i]);
+    if (__ballot(!finite) != 0) {  // the wave's own columns
+#pragma unroll 1
+      for (int f = 0; f < FM * FN; ++f) {
+        f32x4_t x = acc[0][0];
+#pragma unroll
+        for (int j = 1; j < FM * FN; ++j)
+          if (f == j) x = acc[j / FN][j % FN];
+        if (n0 + f % FN * 16 < g.N) w4_exact_fragment<IN, ZEROS, G>(p, t, f / FN * 16, n0 + f % FN * 16, x);
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int m = 0; m < FM; ++m)
 #pragma unroll
@@ -631,26 +644,8 @@ __global__ void __launch_bounds__(256, PER) gemm_w4_panel_kernel(W4Params p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 16 * m + 4 * quarter + i, col = n0 + 16 * n + (lane & 15);
-        const bool good = IN == 1 || is_finite(acc[m][n][i]);
-        if (r < t.rows && col < g.N && good) w4_store<IN>(p, t.row0 + r, col, acc[m][n][i]);
-        finite = finite && good;
+        if (r < t.rows && col < g.N) w4_store<IN>(p, t.row0 + r, col, acc[m][n][i]);
       }
-  if constexpr (IN == 0) {
-    if (__ballot(!finite) != 0) {  // the wave's own columns
-      static_assert(4 * FM * FN <= 32, "a bit for every element of a lane");
-      uint32_t bad = 0;
-#pragma unroll
-      for (int f = 0; f < FM * FN; ++f)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!is_finite(acc[f / FN][f % FN][i]) && w4_in(p, t, f / FN * 16, n0 + f % FN * 16, i)) bad |= 1u << (4 * f + i);
-#pragma unroll 1
-      for (int f = 0; f < FM * FN; ++f) {
-        const uint32_t some = bad >> (4 * f) & 15u;
-        if (__ballot(some != 0) != 0) w4_exact_fragment<IN, ZEROS, G>(p, t, f / FN * 16, n0 + f % FN * 16, some);
-      }
-    }
-  }
 }
 
 }  // namespace tbg
