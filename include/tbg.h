@@ -628,10 +628,15 @@ tbg_status tbg_expert_combine_grad(int64_t tokens, int64_t top_k, int64_t rows, 
 
 /* C <- alpha·A·Wᵀ + beta·C for M rows of activations A (TBG_BF16 or TBG_F16, lda >= K, any alignment of whole
  * elements) and a weight matrix as above; C TBG_F32 or A's type, ldc >= N; it must not overlap the inputs.
- * Per group the sum of A times whole numbers is held in fp32, multiplied by the scale and added in fp32;
- * nothing else is rounded before C, once, to nearest even.  alpha, beta as tbg_gemm_ex.  Made for few rows
- * (the bytes of W are the cost); any number is taken.  For given sizes a row of C depends on its own row of A
- * alone: an infinity or a NaN in another row leaves every bit of it as it is.
+ * Per group the sum of A times whole numbers is held in fp32, multiplied by the scale and added in fp32; C is
+ * rounded once, to nearest even.  For TBG_F16 the whole numbers are code - zero.  For TBG_BF16 they are the
+ * codes, and zero times the group's sum of A is taken off afterwards, also in fp32: what the fp32 sums are off
+ * by goes with S = sum |A|·|scale|·(code + zero), at most (K + 3·K/group + 16)·2^-23·S, and not with
+ * |code - zero|.  Activations of one sign over codes mostly at their zero lose about a digit of fp32 to that, and
+ * a row of W whose codes are all their zero can give a C beside 0; activations around zero do not show it.
+ * For given sizes a row of C depends on its own row of A alone: an infinity or a NaN in another row leaves
+ * every bit of it as it is.
+ * alpha, beta as tbg_gemm_ex.  Made for few rows (the bytes of W are the cost); any number is taken.
  * M == 0 or N == 0 is a no-op; K == 0 gives beta·C.
  * Limits: M up to 2^30, ldb below 2^23 (K up to 2^24 - 32), ld_s and ld_z up to 2^28 (N too), workgroups as for the
  * ragged products.

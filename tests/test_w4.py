@@ -602,3 +602,28 @@ def test_values_near_the_end_of_the_range(M, N):
         assert int(same.sum()) > 100 and torch.equal(got[row][same], exact[row][same])  # whole quarters below 2^20
         rest = [r for r in range(M) if r != row]
         assert torch.equal(got[rest], exact[rest])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N", [(9, 400), (60, 32800)])
+def test_activations_of_one_sign(M, N, dtype):
+    """Codes at or near their zero under activations of one sign: fp16 takes the zero off each code, so its sums are
+    off by their bound over |a|·|s|·|c - z|, and a W of zeros gives zeros; bf16 takes it off the group's sums, with the
+    bound over |a|·|s|·(c + z) that the header states."""
+    ops = _ops()
+    K, G = 1152, 64
+    g = _gen(M + K)
+    a = (torch.randn((M, K), device="cuda", generator=g).clamp(min=0) ** 2).to(TORCH[dtype])
+    s = (0.5 + torch.rand((K // G, N), device="cuda", generator=g)).to(TORCH[dtype])
+    z = torch.randint(0, 16, (K // G, N), device="cuda", generator=g, dtype=torch.uint8)
+    at_zero = z.t().repeat_interleave(G, -1)
+    some = torch.rand((N, K), device="cuda", generator=g) < 0.05
+    code = torch.where(some, torch.randint(0, 16, (N, K), device="cuda", generator=g, dtype=torch.uint8), at_zero)
+    for c in (code, at_zero.contiguous()):
+        w = _weights(c, s, z)
+        exact = a.double() @ w.t().contiguous()
+        got = ops.w4_gemm(a, _pack(c), s, z, out_dtype="f32").double()
+        size = _weights(c, s, z, True) if dtype == "bf16" else w.abs()
+        acc = (K + 3 * (K // G) + 16) * 2.0 ** -23 * (a.double().abs() @ size.t().contiguous())
+        assert bool(((got - exact).abs() <= acc + 2.0 ** -24 * (exact.abs() + acc)).all())

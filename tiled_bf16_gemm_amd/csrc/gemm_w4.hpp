@@ -16,6 +16,10 @@
 //         end of its range that difference may not exist although the definition's sum does: a
 //         result that is not finite is computed again from c - z itself (28 instructions a dword), and
 //         it alone is stored from there, so that what a row holds never shows in another row's bits.
+//         The price of the seven instructions: what the two sums are off by goes with |a|·(c + z), not
+//         with |a|·|c - z|.  K = 4096, squared positive activations, 95 % of the codes at their zero of 7, scale
+//         1: off by up to 4.8e-4 where the values' root mean square is 96 (fp16 0.9e-4, an fp32 product 0.7e-4), and
+//         by 3.2e-4 where every code is 7; activations around zero 3.8e-5 (fp16 4.3e-5).
 //
 // Lane l holds column l%16 of a fragment and 16 bytes, the 32 codes of quarter l/16 of a block of 128.  The
 // product wants the four quarters of 32 codes side by side in a step, so that a step never crosses a group:

@@ -552,7 +552,7 @@ def w4_gemm(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros: O
     (N, K/2) uint8, the lower nibble first, 16-byte aligned and pitched; scales: (K/group, N) of A's type and
     zeros: (K/group, N) uint8 or None (every zero is 8), group 32, 64 or 128:
     W[n, k] = scales[k//group, n]·(code[n, k] - zeros[k//group, n]).  out_dtype: "f32" or A's type; beta != 0
-    needs `out`."""
+    needs `out`.  For bf16 the fp32 sums' error goes with |a|·|scale|·(code + zero) (tbg_w4_gemm)."""
     index = A.get_device()
     (M, Ka), st_a = _require_rows(A, "A", index)
     ab = _AB_OF.get(A.dtype)
