@@ -672,3 +672,143 @@ def test_codes_are_dispatched():
     out = [ops.mx4_gemm_grouped(a, q, bc, bs, off, out=torch.zeros((T * k, N), dtype=torch.bfloat16, device="cuda"))
            for a, q in ((c, s), (c2, s2))]
     assert torch.equal(out[0], out[1])
+
+
+# ---- rows past the cache, and batches of more than one launch -----------------------------------------
+
+def _chunks(n, step=4096):
+    return [slice(i, min(i + step, n)) for i in range(0, n, step)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype,cols,pad", [(torch.uint8, 4099, 0), (torch.bfloat16, 2049, 5), (torch.float32, 1030, 0),
+                                            (torch.float32, 1025, 3)])
+@pytest.mark.parametrize("top_k", [3, 9])
+def test_dispatch_of_rows_past_the_cache(dtype, cols, pad, top_k):
+    """More than 256 MiB of the groups' rows: bit for bit, what lies around them as it was."""
+    x1 = torch.empty(0, dtype=dtype)
+    T = (256 << 20) // (cols * x1.element_size() * top_k) + 50
+    print(f"dispatch {T}x{top_k}, {cols} {dtype}, past the cache", flush=True)
+    _, src, place = _routing(T, top_k, 16, T + cols)
+    n = int((src >= 0).sum())
+    x = torch.randint(-100, 100, (T, cols), device="cuda", generator=_gen(cols)).to(dtype)
+    out = torch.full((T * top_k + 2, cols + pad), 9, device="cuda", dtype=dtype)
+    assert out[1:-1, :cols].numel() * out.element_size() >= 256 << 20
+    _ops().expert_dispatch(_padded(x, cols + 2 * pad, 1) if pad else x, place, out=out[1:-1, :cols])
+    for r in _chunks(n):
+        assert torch.equal(_bits(out[1:-1, :cols][r]), _bits(x[(src[r] // top_k).long()]))
+    assert bool((out[n + 1:] == 9).all()) and bool((out[0] == 9).all()) and bool((out[:, cols:] == 9).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype,out_dtype,cols,pad", [("bf16", "bf16", 2049, 5), ("bf16", "f32", 2048, 0), ("f16", "f16", 2050, 3),
+                                                      ("f16", "f32", 2049, 1), ("f32", "f32", 1026, 1)])
+@pytest.mark.parametrize("top_k", [5, 8, 10])
+def test_combine_of_rows_past_the_cache(dtype, out_dtype, cols, pad, top_k):
+    size = torch.empty(0, dtype=TORCH[dtype]).element_size()
+    T = (256 << 20) // (cols * size * top_k) + 30
+    print(f"combine {T}x{top_k}, {cols} {dtype} -> {out_dtype}, past the cache", flush=True)
+    _, _, place = _routing(T, top_k, 16, T + cols)
+    place[T - 1] = -1
+    y = _padded(torch.randn((T * top_k, cols), device="cuda", generator=_gen(cols)).to(TORCH[dtype]), cols + pad, float("nan"))
+    w = torch.randn((T, top_k), device="cuda", generator=_gen(cols + 1))
+    full = torch.full((T + 2, cols + pad), 9, device="cuda", dtype=TORCH[out_dtype])
+    eps = torch.finfo(TORCH[out_dtype]).eps / 2
+    for weights in (w, None):
+        got = _ops().expert_combine(y, place, weights, out_dtype=out_dtype, out=full[1:-1, :cols])
+        for r in _chunks(T):
+            exact, mag = _combine64(y, place[r], weights[r] if weights is not None else None)
+            bound = (top_k + 1) * 2.0 ** -23 * mag
+            bound = bound + eps * (exact.abs() + bound)
+            if out_dtype == "f16":
+                bound = bound + 2.0 ** -25  # half a step of its subnormals
+            assert bool(((got[r].double() - exact).abs() <= bound).all())
+        assert bool((got[T - 1] == 0).all())
+        assert bool((full[0] == 9).all()) and bool((full[-1] == 9).all()) and bool((full[:, cols:] == 9).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype,d,cols,pad", [("bf16", "bf16", 2049, 5), ("bf16", "f32", 2048, 0), ("f16", "f16", 2050, 3),
+                                              ("f16", "f32", 2049, 1), ("f32", "f32", 1026, 1)])
+@pytest.mark.parametrize("top_k", [2, 4, 5, 9])
+def test_combine_grad_of_rows_past_the_cache(dtype, d, cols, pad, top_k):
+    """Y and dY of more than 256 MiB together: dY bit for bit, the weights' gradient within its sum's bound."""
+    size = torch.empty(0, dtype=TORCH[dtype]).element_size()
+    T = (128 << 20) // (cols * size * top_k) + 30
+    print(f"combine_grad {T}x{top_k}, {cols} {dtype}, dout {d}, past the cache", flush=True)
+    _, src, place = _routing(T, top_k, 16, T + cols)
+    n = int((src >= 0).sum())
+    y = _padded(torch.randn((T * top_k, cols), device="cuda", generator=_gen(cols)).to(TORCH[dtype]), cols + pad, float("nan"))
+    dout = _padded(torch.randn((T, cols), device="cuda", generator=_gen(cols + 1)).to(TORCH[d]), cols + 2 * pad, float("nan"))
+    w = torch.randn((T, top_k), device="cuda", generator=_gen(cols + 2))
+    full = torch.full((T * top_k + 2, cols + pad), 9.0, dtype=TORCH[dtype], device="cuda")
+    dy, dw = _ops().expert_combine_grad(dout, y, place, w, dy=full[1:-1, :cols])
+    dw = dw.flatten()
+    for r in _chunks(n):
+        slot = src[r].long()
+        rows = dout[slot // top_k].float()
+        assert torch.equal(_bits(dy[r]), _bits((w.flatten()[slot][:, None] * rows).to(TORCH[dtype])))
+        terms = y[r].double() * rows.double()
+        assert bool(((dw[slot].double() - terms.sum(1)).abs() <= (cols + 1) * 2.0 ** -23 * terms.abs().sum(1)).all())
+    assert bool((dw[place.flatten() < 0] == 0).all())
+    assert bool((full[n + 1:] == 9).all()) and bool((full[0] == 9).all()) and bool((full[:, cols:] == 9).all())
+
+
+@gpu
+@pytest.mark.parametrize("top_k,cols", [(1, 3), (2, 9)])
+def test_gradients_of_more_tokens_than_a_launch(top_k, cols):
+    """A launch takes 2^22 - 1 tokens: those behind them have their own rows, weights and gradients."""
+    T = (1 << 22) + 2
+    print(f"combine_grad of {T} tokens", flush=True)
+    g = _gen(cols)
+    place = torch.randperm(T * top_k, device="cuda", generator=g).to(torch.int32).reshape(T, top_k)
+    place[T - 3, 0] = place[7, 0] = -1
+    y = torch.randint(-8, 9, (T * top_k, cols), device="cuda", generator=g).half()
+    dout = torch.randint(-8, 9, (T, cols), device="cuda", generator=g).half()
+    w = torch.randint(-8, 9, (T, top_k), device="cuda", generator=g).float()
+    dy, dw = _ops().expert_combine_grad(dout, y, place, w, dy=torch.full_like(y, 99))
+    # whole numbers: products up to 64 and sums up to 576, which fp16 and fp32 hold
+    t, j = (place >= 0).nonzero(as_tuple=True)
+    want = torch.full_like(y, 99)
+    want[place[t, j].long()] = (w[t, j, None] * dout[t].float()).half()
+    assert torch.equal(dy, want)
+    held = place >= 0
+    assert torch.equal(dw, (y[place.clamp(min=0).long()].float() * dout[:, None].float()).sum(-1) * held)
+
+
+def _cut_rows(per_row):
+    """Tokens of one launch, whose 16-byte or single-element units are counted in 32 bits, and some around the cut."""
+    most = ((1 << 32) - 256) // per_row
+    return most, most + 5, [0, 1, most - 2, most - 1, most, most + 1, most + 4]
+
+
+@gpu
+def test_dispatch_of_more_units_than_a_launch():
+    most, T, at = _cut_rows(15)  # rows of 15 bytes go byte by byte
+    print(f"dispatch of {T} tokens", flush=True)
+    x = torch.zeros((T, 15), dtype=torch.uint8, device="cuda")
+    place = torch.full((T, 1), -1, dtype=torch.int32, device="cuda")
+    for i, t in enumerate(at):
+        x[t] = torch.arange(15, device="cuda") + 16 * i + 1
+        place[t] = i + 1
+    out = _ops().expert_dispatch(x, place, out=torch.full((len(at) + 2, 15), 250, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(out[1:-1], x[torch.tensor(at, device="cuda")])
+    assert bool((out[0] == 250).all()) and bool((out[-1] == 250).all())
+
+
+@gpu
+def test_combine_of_more_units_than_a_launch():
+    most, T, at = _cut_rows(7)  # rows of 7 values go one by one
+    print(f"combine of {T} tokens", flush=True)
+    y = torch.randint(1, 9, (len(at), 7), device="cuda", generator=_gen(7)).bfloat16()
+    place = torch.full((T, 1), -1, dtype=torch.int32, device="cuda")
+    w = torch.ones((T, 1), device="cuda")
+    for i, t in enumerate(at):
+        place[t] = i
+        w[t] = i + 1
+    out = torch.full((T, 7), 9, dtype=torch.bfloat16, device="cuda")
+    _ops().expert_combine(y, place, w, out=out)
+    for i, t in enumerate(at):
+        assert torch.equal(out[t], (i + 1) * y[i])  # whole numbers up to 56
+        out[t] = 0
+    assert not any(bool(out[r].any()) for r in _chunks(T, 1 << 26))
