@@ -57,7 +57,24 @@ __device__ __forceinline__ void set_value(Vec<DT, V>& x, int i, float f) {
 }
 
 // Rows of the groups that the last-level cache cannot hold are read and written past it (NT), which leaves
-// it to the rest; those that fit may still be in it, or be read from it next.  launch_* choose by kCacheBytes.
+// it to the rest; those that fit may still be in it, or be read from it next.  That form exists where many rows
+// meet: dispatch to three and more rows a token, combine of five and more, gradients of rows of more than 128 units;
+// those choose by kCacheBytes, the others are cached at any size.  Both sides, µs cached / past the cache, bf16, by
+// MiB of the groups' rows (gradients: of Y and dY), the same buffers call after call:
+//                                      128        256        512        1024
+//   dispatch, 8 KiB rows, 1 a token   35 / 35    91 / 69   184 / 180  368 / 376   cached
+//                         2           26 / 27    72 / 49   142 / 106  290 / 287   cached
+//                         3           23 / 27    69 / 53   140 / 105  275 / 274   by size
+//                         8           22 / 31    49 / 57   121 / 112  250 / 225   by size
+//   combine, 8 KiB rows,  1           36 / 45    95 / 84   191 / 192  378 / 374   cached
+//                         2           27 / 32    71 / 57   142 / 110  282 / 270   cached
+//                         4           25 / 29    60 / 54   124 / 104  252 / 209   cached
+//                         8           25 / 30    53 / 55   116 /  99  239 / 200   by size
+//   gradients, 2 a token, 256 B rows  45 / 61   128 / 121  239 / 225              cached
+//                         2000 B      26 / 33    66 / 64   138 / 116  280 / 233   cached
+//                         8 KiB       23 / 29    72 / 56   127 /  99  254 / 192   by size
+// (The cached kernels lose up to a quarter from 256 MiB on; a form past the cache for two to four rows a token would
+// gain that.)
 // (O names the type, O::type, so that its alignment stays with it.)
 template <int NT, class O>
 __device__ __forceinline__ typename O::type load_from(const uint8_t* at) {
@@ -248,7 +265,7 @@ hipError_t dispatch_units(RowsParams p, hipStream_t s) {
   p.div = make_fast_div(p.per_row);
   return by_tokens(p, [&](RowsParams q, int64_t t, unsigned grid) {
     q.in += t * p.ld_in;
-    // 8192 tokens of 8 KiB, 8 rows each (512 MiB): 126 µs, past the cache 107; 2 rows each (128 MiB): 28 either way
+    // (figures at load_from)
     if (p.top_k <= 2) hipLaunchKernelGGL((dispatch_kernel<SHORT, 2, 0>), dim3(grid), dim3(256), 0, s, q);
     else if (!past_cache(p, 1)) hipLaunchKernelGGL((dispatch_kernel<SHORT, 8, 0>), dim3(grid), dim3(256), 0, s, q);
     else hipLaunchKernelGGL((dispatch_kernel<SHORT, 8, 1>), dim3(grid), dim3(256), 0, s, q);
@@ -261,7 +278,7 @@ hipError_t combine_units(RowsParams p, hipStream_t s) {
   p.div = make_fast_div(p.per_row);
   return by_tokens(p, [&](RowsParams q, int64_t t, unsigned grid) {
     q.out += t * p.ld_out;
-    // 8192 tokens of 8 KiB, 8 rows each (512 MiB): 126 µs, past the cache 109; 2 rows each (128 MiB): 34 and 35
+    // (figures at load_from)
     const bool past = past_cache(p, (int)sizeof(typename Elem<Y>::type));
     if (p.top_k <= 2) hipLaunchKernelGGL((combine_kernel<Y, O, V, 2, 0>), dim3(grid), dim3(256), 0, s, q);
     else if (p.top_k <= 4) hipLaunchKernelGGL((combine_kernel<Y, O, V, 4, 0>), dim3(grid), dim3(256), 0, s, q);
@@ -294,8 +311,8 @@ hipError_t grad_launch(const RowsParams& p, hipStream_t s) {
 }
 
 // Waves a token: one for rows of up to 128 units (2047 tokens, 4 rows of 126 units each: 9.9 µs with one wave, 10.2
-// with two, 11.3 with four), else four (8192 tokens, 2 rows of 512 units: 71, 68, 67).  Past the cache by the rows
-// of Y and dY together: 8192 tokens of 8 KiB, 2 rows each (256 MiB): 67 µs, past the cache 53.
+// with two, 11.3 with four), else four (8192 tokens, 2 rows of 512 units: 71, 68, 67).  Past the cache, where the
+// rows are long, by those of Y and dY together (figures at load_from).
 template <int Y, int D, int V, int J>
 hipError_t grad_rows(const RowsParams& p, hipStream_t s) {
   if (p.per_row <= 128) return grad_launch<Y, D, V, J, 1, 0>(p, s);
