@@ -602,9 +602,10 @@ tbg_status tbg_expert_combine(int64_t tokens, int64_t top_k, int64_t rows, int64
                               int64_t ld_out, tbg_dtype out_dtype, void* stream);
 
 /* The gradients of Y and of the weights under tbg_expert_combine, dout being the gradient of its out:
- *   dY[place[s]]   <- weights[s] * dout[t], rounded once to Y's type.  Rows that no slot holds are left as
- *                     they were; where slots hold the same row (tbg_expert_sort makes none) nothing is
- *                     added up: each of its elements is that of one of them.
+ *   dY[place[s]]   <- weights[s] * dout[t], the fp32 product, rounded to Y's type (both to nearest even).  Rows
+ *                     that no slot holds are left as they were; where slots hold the same row
+ *                     (tbg_expert_sort makes none) nothing is added up: each of its elements is that of one
+ *                     of them.
  *   dweights[s]    <- the sum over the columns of Y[place[s]] * dout[t], held in fp32; 0 for a slot without
  *                     a row.
  *   dout           tokens rows, TBG_F32 or Y's type, ldd >= cols.
