@@ -180,8 +180,10 @@ inline TileChoice choose_mx4(int64_t groups, int64_t M, int64_t N, int64_t K, in
 
 // Rows times weights in 4-bit codes (gemm_w4.hpp), dense (groups == 0) or ragged.  The panel kernel (128 columns
 // and 16, 32 or 64 rows a workgroup, A in LDS) needs a workgroup for every CU; below that the waves of a workgroup of
-// 16 rows split K, over as many columns (64, 32, 16) as leave most of the CUs a workgroup.  µs, K = 4096, group 128,
-// bf16, by rows × columns; split K with 16, 32, 64 columns, then panels of 16, 32, 64 rows:
+// 16 rows split K, over as many columns (64, 32, 16) as leave most of the CUs a workgroup.  One limit serves every
+// group: at 32 × 14336 it leaves 21.0 for 19.4 µs in groups of 128, where the panel would take 28.6 for 23.0 in groups
+// of 32 with zeros.  µs, K = 4096, group 128, bf16, by rows × columns; split K with 16, 32, 64 columns, then panels
+// of 16, 32, 64 rows:
 //     1 ×  4096    5.1   6.1   8.3   17.9  23.0  34.1        64 ×  4096   23.6  16.3  12.4   19.0  24.3  36.2
 //     1 × 14336   12.5  10.6  10.0   18.7  23.8  35.0        64 ×  8192   44.0  28.5  21.2   19.5  24.4  36.1
 //    16 × 14336   23.4  16.4  12.8   19.0  23.9  35.3        64 × 14336   75.9  47.8  37.6   26.1  24.6  36.0
