@@ -627,3 +627,27 @@ def test_activations_of_one_sign(M, N, dtype):
         size = _weights(c, s, z, True) if dtype == "bf16" else w.abs()
         acc = (K + 3 * (K // G) + 16) * 2.0 ** -23 * (a.double().abs() @ size.t().contiguous())
         assert bool(((got - exact).abs() <= acc + 2.0 ** -24 * (exact.abs() + acc)).all())
+
+
+# ---- the layout as the README fills it ----------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("N,K,group", [(50, 160, 32), (33, 256, 128), (64, 192, 64)])
+def test_readme_quantises_and_multiplies(N, K, group):
+    """The README's lines: W comes back within half a step of its group and what the scale's rounding adds, and the
+    product is W's."""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    block = next(b for b in open(os.path.join(root, "README.md")).read().split("```python\n")[1:] if "w4_gemm(" in b)
+    g = _gen(N)
+    env = dict(torch=torch, N=N, K=K, group=group, w=torch.randn((N, K), device="cuda", generator=g),
+               x=torch.randn((7, K), device="cuda", generator=g).bfloat16())
+    exec(block.split("```")[0], env)
+    code, scales, zeros = env["code"], env["scales"], env["zeros"]
+    w = _weights(code, scales, zeros)
+    steps = scales.double().t().repeat_interleave(group, -1)
+    # a code is off by half a step; at the upper end, where it ends at 15, by half a step of the zero's rounding and
+    # by the 15·2^-8 / (1 - 2^-8) steps that a scale rounded down to bf16 leaves out (1e-3: the fp32 quotients)
+    assert bool(((w - env["w"].double()).abs() <= (0.5 + 15 / 255 + 1e-3) * steps).all())
+    exact = env["x"].double() @ w.t().contiguous()
+    assert bool(((env["y"].double() - exact).abs() <= _bound(env["x"], code, scales, zeros, exact, "bf16")).all())
