@@ -812,3 +812,38 @@ def test_combine_of_more_units_than_a_launch():
         assert torch.equal(out[t], (i + 1) * y[i])  # whole numbers up to 56
         out[t] = 0
     assert not any(bool(out[r].any()) for r in _chunks(T, 1 << 26))
+
+
+@gpu
+@pytest.mark.parametrize("dtype,cols", [(torch.uint8, 15), (torch.float16, 7), (torch.float32, 3)])
+def test_dispatch_of_short_rows_past_the_cache(dtype, cols):
+    """More than 256 MiB of rows below 16 bytes, which go element by element."""
+    size, k = torch.empty(0, dtype=dtype).element_size(), 3
+    T = (256 << 20) // (cols * size * k) + 3
+    print(f"dispatch {T}x{k}, {cols} {dtype}, past the cache", flush=True)
+    place = torch.randperm(T * k, device="cuda", generator=_gen(cols)).to(torch.int32).reshape(T, k)
+    place[5, 1] = place[T - 1, 2] = -1
+    x = torch.randint(0, 100, (T, cols), device="cuda", generator=_gen(cols + 1)).to(dtype)
+    want = torch.full((T * k, cols), 101, device="cuda").to(dtype)
+    t, j = (place >= 0).nonzero(as_tuple=True)
+    want[place[t, j].long()] = x[t]
+    got = _ops().expert_dispatch(x, place, out=torch.full((T * k, cols), 101, device="cuda").to(dtype))
+    assert torch.equal(_bits(got), _bits(want))
+
+
+@gpu
+@pytest.mark.parametrize("dtype,out_dtype,cols", [("bf16", "bf16", 7), ("bf16", "f32", 5), ("f16", "f16", 7), ("f16", "f32", 3),
+                                                  ("f32", "f32", 3)])
+def test_combine_of_short_rows_past_the_cache(dtype, out_dtype, cols):
+    """The same way back, in whole numbers: sums up to 5·8·8 are exact in every type but bf16, which rounds them once."""
+    size, k = torch.empty(0, dtype=TORCH[dtype]).element_size(), 5
+    T = (256 << 20) // (cols * size * k) + 3
+    print(f"combine {T}x{k}, {cols} {dtype} -> {out_dtype}, past the cache", flush=True)
+    place = torch.randperm(T * k, device="cuda", generator=_gen(cols)).to(torch.int32).reshape(T, k)
+    place[5, 1] = place[T - 1, 2] = -1
+    y = torch.randint(-8, 9, (T * k, cols), device="cuda", generator=_gen(cols + 1)).to(TORCH[dtype])
+    w = torch.randint(-8, 9, (T, k), device="cuda", generator=_gen(cols + 2)).float()
+    got = _ops().expert_combine(y, place, w, out_dtype=out_dtype)
+    for r in _chunks(T, 1 << 20):
+        terms = w[r][..., None] * (place[r] >= 0)[..., None] * y[place[r].clamp(min=0).long()].float()
+        assert torch.equal(got[r], terms.sum(1).to(TORCH[out_dtype]))
